@@ -27,8 +27,10 @@ ERR_RECORD_BYTES = 256
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 U8ROW = 3   # row-wise 8-bit table records (tables only)
-DT_CODE = {"f32": F32, "f16": F16, "bf16": BF16, "u8row": U8ROW, torch.float32: F32, torch.float16: F16,
-           torch.bfloat16: BF16, torch.uint8: U8ROW}
+E4M3 = 4    # 8-bit floating point rows with a scale each (dlrm_rmsnorm_fwd's output, dlrm_experts_fwd's operands)
+MAX_EXPERTS = 256
+DT_CODE = {"f32": F32, "f16": F16, "bf16": BF16, "u8row": U8ROW, "e4m3": E4M3, torch.float32: F32, torch.float16: F16,
+           torch.bfloat16: BF16, torch.uint8: U8ROW, torch.float8_e4m3fn: E4M3}
 DT_TORCH = {F32: torch.float32, F16: torch.float16, BF16: torch.bfloat16}
 
 
@@ -115,6 +117,28 @@ _SIGS = {
     "dlrm_gemm_tf32x3": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_void_p,
                                    C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p, C.c_size_t,
                                    C.c_void_p]),
+    "dlrm_embed_fwd": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_void_p, C.c_float, C.c_void_p, C.c_int64, C.c_int,
+                                 C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dlrm_embed_bwd_workspace_size": (C.c_size_t, [C.c_int64, C.c_int, C.c_int64]),
+    "dlrm_embed_bwd": (C.c_int, [C.c_int64, C.c_int, C.c_int64, C.c_void_p, C.c_float, C.c_void_p, C.c_int64, C.c_int,
+                                 C.c_void_p, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dlrm_dropout": (C.c_int, [C.c_int64, C.c_void_p, C.c_void_p, C.c_int, C.c_double, C.c_void_p, C.c_void_p,
+                               C.c_void_p]),
+    "dlrm_rmsnorm_fwd": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int, C.c_void_p,
+                                   C.c_float, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int, C.c_void_p,
+                                   C.c_void_p, C.c_void_p]),
+    "dlrm_rmsnorm_bwd_workspace_size": (C.c_size_t, [C.c_int, C.c_int]),
+    "dlrm_rmsnorm_bwd": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_int64, C.c_void_p,
+                                   C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dlrm_experts_fwd": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p,
+                                   C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int, C.c_void_p,
+                                   C.c_int64, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dlrm_experts_bwd_workspace_size": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]),
+    "dlrm_experts_bwd": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p,
+                                   C.c_int64, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int,
+                                   C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_int64, C.c_int, C.c_void_p,
+                                   C.c_void_p, C.c_size_t, C.c_void_p]),
 }
 
 
@@ -483,6 +507,221 @@ def dlrm_backward_pooled(K: int, d: int, bot: MLP, top: MLP, B: int, dense, pool
 def dlrm_mlp_sgd(K: int, d: int, bot: MLP, top: MLP, B: int, lr: float, grads, stream=None):
     return _check(lib().dlrm_mlp_sgd(int(K), int(d), bot.ref(), top.ref(), int(B), float(lr), _ptr(grads),
                                      _nbytes(grads), _stream(stream)), "dlrm_mlp_sgd")
+
+
+# ----------------------------------------------------------------- token blocks
+
+# These calls take their sizes, types and row pitches from the tensors. Every tensor of a call is on one CUDA
+# device; the call runs on that device's current stream unless it is given one.
+
+def _refuse(where: str, status: int = ERR_INVALID_ARG):
+    raise DlrmError(status, where)
+
+
+def _matrix(t, where: str, rows: int, cols: int):
+    """(pointer, row pitch) of a [rows][cols] tensor whose rows are contiguous."""
+    if t is None:
+        return None, cols
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        _refuse(where)
+    # the pitch of a single row says nothing: any pitch that keeps the alignment rules will do
+    return _ptr(t), (t.stride(0) if rows > 1 else (cols + 15) // 16 * 16)
+
+
+def _stacked(t, where: str, n: int, rows: int, cols: int):
+    """(pointer, row pitch) of [n][rows][cols] whose matrices follow one another at rows * pitch."""
+    if t is None:
+        return None, cols
+    if t.dim() != 3 or tuple(t.shape) != (n, rows, cols) or (cols > 1 and t.stride(2) != 1):
+        _refuse(where)
+    if rows > 1:
+        ld = t.stride(1)
+    else:
+        ld = t.stride(0) if n > 1 else (cols + 15) // 16 * 16
+    if n > 1 and t.stride(0) != rows * ld:
+        _refuse(where)
+    return _ptr(t), ld
+
+
+def _vector(t, where: str, dtype, n: int, needed: bool = False):
+    """Pointer of a dense tensor of n elements of one type (None passes unless needed)."""
+    if t is None:
+        if needed:
+            _refuse(where)
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        _refuse(where)
+    return _ptr(t)
+
+
+def _float_code(t, where: str) -> int:
+    code = DT_CODE.get(t.dtype)
+    if code not in (F32, F16, BF16):
+        _refuse(where)
+    return code
+
+
+def _same_device(where: str, *tensors):
+    """The one CUDA device every given tensor is on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or (dev is not None and t.device != dev):
+            _refuse(where)
+        dev = t.device
+    return dev
+
+
+def _call(where: str, dev, stream, fn, *args):
+    """Runs a C entry point on the tensors' device, which need not be the current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != dev:
+            _refuse(where)
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        return _check(fn(*args, C.c_void_p(int(stream))), where)
+    with torch.cuda.device(dev):
+        return _check(fn(*args, C.c_void_p(int(stream))), where)
+
+
+def dlrm_embed_fwd(T: Tables, k: int, indices, out, ws, scale: float = 1.0, stream=None):
+    """out[i] = scale * row indices[i] of table k (zeros, and counted in ws, for an index outside it).
+    indices: int32 [n]; out: [n][d], fp32, fp16 or bf16."""
+    f = "dlrm_embed_fwd"
+    n = indices.numel()
+    idx = _vector(indices, f, torch.int32, n)
+    ptr, ld = _matrix(out, f, n, T.d)
+    if not 0 <= int(k) < T.K or T.data.numel() < sum(T.rows) * (T.d if T.struct.dt != U8ROW else 1):
+        _refuse(f)
+    dev = _same_device(f, T.data, indices, out, ws)
+    return _call(f, dev, stream, lib().dlrm_embed_fwd, T.ref(), int(k), n, idx, float(scale), ptr, ld,
+                 _float_code(out, f), _ptr(ws), _nbytes(ws))
+
+
+def dlrm_embed_bwd_workspace_size(rows: int, d: int, n: int) -> int:
+    return int(lib().dlrm_embed_bwd_workspace_size(int(rows), int(d), int(n)))
+
+
+def dlrm_embed_bwd(indices, dout, dtable, ws, scale: float = 1.0, stream=None):
+    """dtable[r] = scale * sum of dout[i] over indices[i] == r, for every row (zeros where there is none).
+    indices: int32 [n]; dout: [n][d]; dtable: dense [rows][d]."""
+    f = "dlrm_embed_bwd"
+    n = indices.numel()
+    if dtable.dim() != 2 or not dtable.is_contiguous():
+        _refuse(f)
+    rows, d = dtable.shape
+    idx = _vector(indices, f, torch.int32, n)
+    ptr, ld = _matrix(dout, f, n, d)
+    dev = _same_device(f, indices, dout, dtable, ws)
+    return _call(f, dev, stream, lib().dlrm_embed_bwd, rows, d, n, idx, float(scale), ptr, ld, _float_code(dout, f),
+                 _ptr(dtable), _float_code(dtable, f), _ptr(ws), _nbytes(ws))
+
+
+def dlrm_dropout(x, y, p: float, rng, residual=None, stream=None):
+    """y = [residual +] (kept ? x / (1 - p) : 0), element by element; rng: device int64 [2], {seed, offset}.
+    The same call on the gradient (without residual) is the backward pass. x, residual and y are dense and of
+    one type; y may be x or residual."""
+    f = "dlrm_dropout"
+    n = x.numel()
+    if residual is not None and residual.shape != x.shape or y.shape != x.shape:
+        _refuse(f)
+    args = (_vector(x, f, x.dtype, n), _vector(residual, f, x.dtype, n), _float_code(x, f), float(p),
+            _vector(rng, f, torch.int64, 2, True), _vector(y, f, x.dtype, n))
+    dev = _same_device(f, x, residual, rng, y)
+    return _call(f, dev, stream, lib().dlrm_dropout, n, *args)
+
+
+def dlrm_rmsnorm_fwd(x, w, y, eps: float = 1e-6, residual=None, h=None, y_scale=None, rstd=None, stream=None):
+    """h = x + residual; rstd = 1 / sqrt(mean(h^2) + eps); y = h * rstd * w, by rows of x [rows][d].
+    y is of x's type, or float8_e4m3fn with y_scale (fp32 [rows]); w: fp32 [d] or None; h and rstd (fp32
+    [rows]) are what the backward pass takes."""
+    f = "dlrm_rmsnorm_fwd"
+    if x.dim() != 2:
+        _refuse(f)
+    rows, d = x.shape
+    for t in (residual, h):
+        if t is not None and t.dtype != x.dtype:
+            _refuse(f)
+    code, ycode = _float_code(x, f), DT_CODE.get(y.dtype)
+    if ycode not in (code, E4M3):
+        _refuse(f)
+    (px, lx), (pr, lr), (ph, lh), (py, ly) = (_matrix(t, f, rows, d) for t in (x, residual, h, y))
+    args = (_vector(w, f, torch.float32, d), float(eps), ph, lh, py, ly, ycode,
+            _vector(y_scale, f, torch.float32, rows, ycode == E4M3 and rows > 0), _vector(rstd, f, torch.float32, rows))
+    if y_scale is not None and ycode != E4M3:
+        _refuse(f)
+    if rows == 0:
+        return OK
+    dev = _same_device(f, x, w, y, residual, h, y_scale, rstd)
+    return _call(f, dev, stream, lib().dlrm_rmsnorm_fwd, rows, d, px, lx, pr, lr, code, *args)
+
+
+def dlrm_rmsnorm_bwd_workspace_size(rows: int, d: int) -> int:
+    return int(lib().dlrm_rmsnorm_bwd_workspace_size(int(rows), int(d)))
+
+
+def dlrm_rmsnorm_bwd(dy, h, rstd, w, dx, ws, dw=None, dh=None, stream=None):
+    """dx (of x and of residual alike) and dw (fp32 [d]) of dlrm_rmsnorm_fwd from its h and rstd; dh: the
+    gradient that reaches h by other ways. dx may be dy or dh."""
+    f = "dlrm_rmsnorm_bwd"
+    if dy.dim() != 2:
+        _refuse(f)
+    rows, d = dy.shape
+    for t in (h, dx, dh):
+        if t is not None and t.dtype != dy.dtype:
+            _refuse(f)
+    (py, ly), (ph, lh), (pd, ld), (px, lx) = (_matrix(t, f, rows, d) for t in (dy, h, dh, dx))
+    args = (_vector(rstd, f, torch.float32, rows, True), _vector(w, f, torch.float32, d), pd, ld, _float_code(dy, f), px,
+            lx, _vector(dw, f, torch.float32, d), _ptr(ws), _nbytes(ws))
+    dev = _same_device(f, dy, h, rstd, w, dx, dw, dh, ws)
+    return _call(f, dev, stream, lib().dlrm_rmsnorm_bwd, rows, d, py, ly, ph, lh, *args)
+
+
+def _experts_sizes(X, W, offsets, where: str):
+    if X.dim() != 2 or W.dim() != 3 or X.shape[1] != W.shape[2] or X.dtype != W.dtype:
+        _refuse(where)
+    n_exp, N, K = W.shape
+    return n_exp, X.shape[0], N, K, _vector(offsets, where, torch.int32, n_exp + 1, True)
+
+
+def dlrm_experts_fwd(X, W, offsets, Y, ws, bias=None, act: int = ACT_NONE, x_scale=None, w_scale=None, stream=None):
+    """Y[r] = act(X[r] W[e]^T + bias[e]) for the rows r in [offsets[e], offsets[e + 1]) of every expert e; other
+    rows of Y are left as they are. X: [M][K], W: [E][N][K] of fp16, bf16, or float8_e4m3fn with x_scale (fp32
+    [M]) and w_scale (fp32 [E][N]); offsets: int32 [E + 1] on the device; Y: [M][N] of X's type or fp32
+    (8-bit operands: fp32, fp16 or bf16); bias: fp32 [E][N]."""
+    f = "dlrm_experts_fwd"
+    n_exp, M, N, K, offs = _experts_sizes(X, W, offsets, f)
+    (px, lx), (py, ly) = _matrix(X, f, M, K), _matrix(Y, f, M, N)
+    pw, lw = _stacked(W, f, n_exp, N, K)
+    code = DT_CODE.get(X.dtype, -1)
+    args = (_vector(x_scale, f, torch.float32, M), code, pw, lw, _vector(w_scale, f, torch.float32, n_exp * N),
+            _vector(bias, f, torch.float32, n_exp * N), int(act), py, ly, _float_code(Y, f), _ptr(ws), _nbytes(ws))
+    dev = _same_device(f, X, W, offsets, Y, ws, bias, x_scale, w_scale)
+    return _call(f, dev, stream, lib().dlrm_experts_fwd, n_exp, M, N, K, offs, px, lx, *args)
+
+
+def dlrm_experts_bwd_workspace_size(n_experts: int, M: int, N: int, K: int, act: int = ACT_NONE) -> int:
+    return int(lib().dlrm_experts_bwd_workspace_size(int(n_experts), int(M), int(N), int(K), int(act)))
+
+
+def dlrm_experts_bwd(dY, X, W, offsets, ws, Y=None, act: int = ACT_NONE, dX=None, dW=None, db=None, stream=None):
+    """Gradients of dlrm_experts_fwd (fp16 or bf16): dX [M][K] (rows outside every range are left as they are),
+    dW [E][N][K], both of X's type or fp32, and db (fp32 [E][N]); each optional. Y: the forward's output, needed
+    for ACT_RELU."""
+    f = "dlrm_experts_bwd"
+    n_exp, M, N, K, offs = _experts_sizes(X, W, offsets, f)
+    if dY.dtype != X.dtype or (Y is not None and Y.dtype != X.dtype) or (act == ACT_RELU and Y is None):
+        _refuse(f)
+    (pdy, ldy), (py, ly), (px, lx), (pdx, ldx) = (_matrix(t, f, M, c) for t, c in ((dY, N), (Y, N), (X, K), (dX, K)))
+    (pw, lw), (pdw, ldw) = _stacked(W, f, n_exp, N, K), _stacked(dW, f, n_exp, N, K)
+    args = (pdy, ldy, py, ly, int(act), px, lx, pw, lw, DT_CODE.get(X.dtype, -1), pdx, ldx,
+            F32 if dX is None else _float_code(dX, f), pdw, ldw, F32 if dW is None else _float_code(dW, f),
+            _vector(db, f, torch.float32, n_exp * N), _ptr(ws), _nbytes(ws))
+    dev = _same_device(f, dY, X, W, offsets, ws, Y, dX, dW, db)
+    return _call(f, dev, stream, lib().dlrm_experts_bwd, n_exp, M, N, K, offs, *args)
 
 
 def grads_view(grads: torch.Tensor, off: int, shape) -> torch.Tensor:

@@ -283,7 +283,7 @@ dlrm_status dlrm_set_wait_polls(int64_t polls) {
 }
 
 int dlrm_ld(int n, dlrm_dtype dt) {
-    const int per = 16 / (int)esize(dt);
+    const int per = dt == DLRM_E4M3 ? 16 : 16 / (int)esize(dt);
     return (n + per - 1) / per * per;
 }
 

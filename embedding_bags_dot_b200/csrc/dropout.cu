@@ -1,0 +1,139 @@
+// Dropout with a counter-based generator: y = [residual +] keep * x / (1 - p).
+//
+// No mask is stored: whether element i is kept follows from (seed, offset, i)
+// alone, so the backward pass is the same call on the gradient. Elements 4 g
+// .. 4 g + 3 take the four 32-bit words of Philox4x32-10 (Salmon, Moraes, Dror
+// and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) with counter
+// {g, g >> 32, offset, offset >> 32} and key {seed, seed >> 32}; an element is
+// kept when its word is at least p * 2^32 (rounded to an integer), so the
+// probability is right to 2^-33.
+//
+// Bound by memory at the larger sizes (2 or 3 arrays read and written once)
+// and by the integer pipe close behind it: ten rounds of two 32 x 32 -> 64
+// products serve four elements. Each thread takes runs of 16 bytes (four or
+// eight elements, one or two generator calls). seed and offset are read from
+// device memory so that a captured graph draws anew when they are changed
+// between replays.
+#include "kernels.cuh"
+#include "rowvec.cuh"
+
+namespace dlrm {
+namespace {
+
+__device__ __forceinline__ uint4 philox4x32_10(unsigned long long group, uint32_t c2, uint32_t c3, uint32_t k0,
+                                               uint32_t k1) {
+    uint32_t c0 = (uint32_t)group, c1 = (uint32_t)(group >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const unsigned long long a = (unsigned long long)0xD2511F53u * c0;
+        const unsigned long long b = (unsigned long long)0xCD9E8D57u * c2;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c1 = (uint32_t)b;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+
+struct DropArgs {
+    long long n;
+    const void* x;
+    const void* residual;       // or null
+    void* y;
+    const unsigned long long* rng;   // {seed, offset}
+    uint32_t threshold;              // kept when word >= threshold ...
+    bool any;                        // ... unless p * 2^32 rounds to 2^32: nothing is kept
+    float scale;
+};
+
+// VEC = elements per 16 bytes, or 4 with element-wise accesses (ALIGNED = false).
+template <typename T, bool RES, bool ALIGNED>
+__global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ DropArgs a) {
+    pdl_wait();
+    constexpr int VEC = ALIGNED ? 16 / (int)sizeof(T) : 4;
+    const T* x = static_cast<const T*>(a.x);
+    const T* res = static_cast<const T*>(a.residual);
+    T* y = static_cast<T*>(a.y);
+    const unsigned long long seed = a.rng[0], off = a.rng[1];
+    const uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32), c2 = (uint32_t)off, c3 = (uint32_t)(off >> 32);
+    const long long stride = (long long)gridDim.x * blockDim.x * VEC;
+    for (long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * VEC; i < a.n; i += stride) {
+        const bool whole = ALIGNED && i + VEC <= a.n;
+        RowRaw<T, VEC> rx, rr;
+        if (whole) {
+            rx.load(x + i);
+            if constexpr (RES) rr.load(res + i);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (i + e < a.n) {
+                    rx.e[e] = x[i + e];
+                    if constexpr (RES) rr.e[e] = res[i + e];
+                }
+        }
+        float v[VEC];
+#pragma unroll
+        for (int g = 0; g < VEC / 4; ++g) {
+            const uint4 w = philox4x32_10((unsigned long long)(i / 4 + g), c2, c3, k0, k1);
+            const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // a dropped element gives zero whatever x holds there (infinity and NaN too)
+                const int q = 4 * g + e;
+                v[q] = word[e] >= a.threshold && a.any ? Cvt<T>::to_f(rx.e[q]) * a.scale : 0.f;
+                if constexpr (RES) v[q] += Cvt<T>::to_f(rr.e[q]);
+            }
+        }
+        RowRaw<T, VEC> out;
+        out.set(v);
+        if (whole) {
+            out.store(y + i);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (i + e < a.n) y[i + e] = out.e[e];
+        }
+    }
+}
+
+template <typename T>
+dlrm_status launch_t(const DropArgs& a, cudaStream_t st) {
+    const bool al = rows_on(a.x, 0, 16) && rows_on(a.y, 0, 16) && rows_on(a.residual, 0, 16);
+    const int vec = al ? 16 / (int)sizeof(T) : 4;
+    const long long want = (a.n + 256ll * vec - 1) / (256ll * vec);
+    const long long most = 16ll * device_sms();
+    const dim3 grid((unsigned)(want < most ? want : most));
+#define DLRM_DROP(RES, AL) DLRM_PDL_CHECK(launch_pdl(dropout_kernel<T, RES, AL>, grid, dim3(256), 0, st, a))
+    if (a.residual) {
+        if (al) DLRM_DROP(true, true);
+        else DLRM_DROP(true, false);
+    } else {
+        if (al) DLRM_DROP(false, true);
+        else DLRM_DROP(false, false);
+    }
+#undef DLRM_DROP
+    return DLRM_OK;
+}
+
+}  // namespace
+
+dlrm_status launch_dropout(long long n, const void* x, const void* residual, dlrm_dtype dt, double p,
+                           const int64_t* rng, void* y, cudaStream_t st) {
+    DropArgs a;
+    a.n = n;
+    a.x = x;
+    a.residual = residual;
+    a.y = y;
+    a.rng = reinterpret_cast<const unsigned long long*>(rng);
+    const double t = p * 4294967296.0 + 0.5;
+    a.any = t < 4294967296.0;
+    a.threshold = a.any ? (uint32_t)t : 0u;
+    a.scale = a.any ? (float)(1.0 / (1.0 - p)) : 0.f;
+    if (dt == DLRM_F32) return launch_t<float>(a, st);
+    if (dt == DLRM_F16) return launch_t<__half>(a, st);
+    return launch_t<__nv_bfloat16>(a, st);
+}
+
+}  // namespace dlrm

@@ -1,0 +1,1048 @@
+// Products grouped by expert, ragged: expert e owns rows [offsets[e],
+// offsets[e + 1]) of the activations and one weight matrix W_e [N][K].
+//   forward  Y  = act(X W_e^T + b_e)      per row          A = X  (K),  B = W_e (K)
+//   dgrad    dX = dP W_e                  per row          A = dP (K),  B = W_e (MN)
+//   wgrad    dW_e = dP_e^T X_e            over e's rows    A = dP (MN), B = X   (MN)
+// with dP = dY where the forward's output is positive (ReLU) or dY itself.
+// Operands are 16-bit (fp16 or bf16), the forward also e4m3 with one fp32
+// scale per row of X and per row of W; accumulation is fp32.
+//
+// The offsets stay on the device: every CTA reads them after the previous
+// kernel, checks them, and walks the same list of tiles (experts in order,
+// then row blocks, then column blocks), taking every gridDim-th one. A row
+// block past its expert's end multiplies rows of the next expert (or zeros)
+// into accumulator rows that are never stored: rows do not mix. In wgrad rows
+// are the reduction, so an expert's last, incomplete 64-row block is read from
+// a copy padded with zeros (expert_prep_kernel), and no other row's infinity
+// or NaN can reach it. Weights are three-dimensional tensor maps, so a block
+// past row N of W_e reads zeros, not the next expert's weights.
+//
+// Two kernels on tcgen05 with TMA-fed 128-byte-swizzled shared memory:
+//  - expert_pair_kernel: 256 x 256 tiles on SM pairs (cta_group::2), all three
+//    products. Bound by the tensor pipe at large sizes.
+//  - expert_tile_kernel: 128 x 64 or 128 x 128 tiles on one SM, forward only, for
+//    calls too small to fill the pairs; with few rows the weights are all the
+//    traffic and narrow tiles put more SMs to reading them. A row block of at
+//    most 32 rows loads 32 rows instead of 128.
+// The tensor core truncates as it accumulates, so no accumulator runs longer
+// than 8 k-blocks (512 16-bit or 1,024 8-bit terms): the epilogue warps add each
+// finished part to fp32 registers, rounding to nearest, while the next part
+// accumulates in the other TMEM buffer.
+// All waits are bounded: on timeout the kernel records DLRM_ERR_TIMEOUT, drains
+// its copies and MMAs (again bounded), frees TMEM and returns. No multicast load.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "kernels.cuh"
+#include "rowvec.cuh"
+#include "tcgen05.cuh"
+
+namespace dlrm {
+namespace tc {
+
+constexpr int EX_MAX = DLRM_MAX_EXPERTS;
+constexpr int PART = 8;                             // k-blocks per accumulator
+constexpr int EX_THREADS2 = 384;                    // pair kernel: warps 0..3 TMA, MMA, idle; 4..11 epilogue
+constexpr int EX_REGS_LOW = 40, EX_REGS_HIGH = 232;
+static_assert(128 * EX_REGS_LOW + 256 * EX_REGS_HIGH <= 168 * EX_THREADS2, "register split exceeds the launch allocation");
+constexpr int EX_STAGES2 = 6;
+constexpr int EX_STAGE2_BYTES = 32768;              // 128 rows x 128 bytes of A, as much of B
+
+enum ExpertOp { EX_FWD = 0, EX_DGRAD = 1, EX_WGRAD = 2 };
+enum ExpertKind { EX_F16 = 0, EX_F8 = 1 };
+
+struct ExpertArgs {
+    int E, M;                 // experts; rows of the activations
+    int J;                    // output columns: N (fwd), K (dgrad), K (wgrad)
+    int I;                    // wgrad: output rows per expert (N)
+    int R;                    // reduction length of fwd (K) and dgrad (N)
+    const int32_t* offsets;
+    bool count;               // whether this launch reports bad ranges
+    const float* bias;        // fwd, or null: [E][J]
+    const float* x_scale;     // e4m3: [M]
+    const float* w_scale;     // e4m3: [E][J]
+    bool relu;
+    void* C;
+    long long ldc;
+    ErrRecord* err;
+};
+
+struct ExpertMaps {
+    CUtensorMap a, b, c;
+    CUtensorMap a32;          // tile kernel: 32-row boxes of A
+    CUtensorMap at, bt;       // wgrad: zero-padded last blocks
+};
+
+struct Ranges {
+    int begin[EX_MAX];
+    int end[EX_MAX];
+};
+
+template <int NS>
+struct ExBars {
+    unsigned long long full[NS];
+    unsigned long long empty[NS];
+    unsigned long long tfull[2];
+    unsigned long long tempty[2];
+    unsigned long long drain;
+    unsigned int tmem_base;
+    int abort;
+};
+
+// One warp fills the ranges. An expert whose range decreases, leaves [0, M] or starts before an earlier offset
+// has no rows (and is counted), so ranges never overlap.
+__device__ __forceinline__ void read_ranges(const ExpertArgs& a, Ranges* rg, bool count) {
+    const int lane = threadIdx.x & 31;
+    const int per = (a.E + 31) / 32;
+    const int e0 = lane * per < a.E ? lane * per : a.E, e1 = e0 + per < a.E ? e0 + per : a.E;
+    int most = 0;                 // largest offset in [e0, e1)
+    for (int e = e0; e < e1; ++e) most = max(most, a.offsets[e]);
+    int before = most;            // inclusive scan, then shifted: the largest offset before e0
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before = max(before, up);
+    }
+    before = __shfl_up_sync(0xffffffffu, before, 1);
+    if (lane == 0) before = 0;
+    unsigned bad = 0;
+    for (int e = e0; e < e1; ++e) {
+        const int s = a.offsets[e], t = a.offsets[e + 1];
+        const bool ok = s >= before && t >= s && t <= a.M;
+        before = max(before, s);
+        bad += !ok;
+        rg->begin[e] = ok ? s : 0;
+        rg->end[e] = ok ? t : 0;
+    }
+    if (count) report_warp(a.err, 0, bad);
+}
+
+// Position in the list of tiles: experts in order, `per` column blocks for each of an expert's row blocks
+// (a fixed number of tiles per expert in wgrad).
+struct TileWalk {
+    const Ranges* rg;
+    int E, nb;                // experts; column blocks
+    int rows_per;             // rows per row block; 0: `fixed` row blocks per expert
+    int fixed;
+    int e = 0;
+    long long base = 0;       // tiles before expert e
+    __device__ __forceinline__ long long tiles() const {
+        const long long rb = rows_per ? (rg->end[e] - rg->begin[e] + rows_per - 1) / rows_per : fixed;
+        return rb * nb;
+    }
+    // Moves on to the expert of tile t (t never decreases); false past the last tile.
+    __device__ __forceinline__ bool seek(long long t, int& mb, int& cb) {
+        while (e < E) {
+            const long long n = tiles();
+            if (t < base + n) {
+                const int local = (int)(t - base);
+                mb = local / nb;
+                cb = local - mb * nb;
+                return true;
+            }
+            base += n;
+            ++e;
+        }
+        return false;
+    }
+};
+
+// MN-major 16-bit operand with 128-byte swizzle: each reduction row is 128 bytes (64 consecutive M/N elements),
+// 8-row groups are 1,024 bytes apart, 64-wide M/N blocks one 64-row box (8 KB) apart.
+__device__ __forceinline__ uint64_t sdesc_mn16(uint32_t addr) {
+    uint64_t d = (uint64_t)((addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(8192 >> 4) << 16;   // leading byte offset: next 64-wide M/N block
+    d |= (uint64_t)(1024 >> 4) << 32;   // stride byte offset: next 8 reduction rows
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Instruction descriptor: fp32 accumulate; fmt: f16 kind 0 = fp16, 1 = bf16; f8f6f4 kind 0 = e4m3.
+__host__ __device__ constexpr uint32_t ex_idesc(int fmt, bool a_mn, bool b_mn, int m, int n) {
+    return (1u << 4) | ((uint32_t)fmt << 7) | ((uint32_t)fmt << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+template <int KIND, int CG>
+__device__ __forceinline__ void ex_umma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
+    if constexpr (KIND == EX_F16 && CG == 2) {
+        umma2(d, a, b, id, accum);
+    } else if constexpr (KIND == EX_F16) {
+        umma(d, a, b, id, accum);
+    } else if constexpr (CG == 2) {
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(accum));
+    } else {
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(accum));
+    }
+}
+
+__device__ __forceinline__ void ex_load_3d(uint32_t dst, const CUtensorMap* map, unsigned long long* bar, int x, int y,
+                                           int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(su32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void ex_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t leader_bar, int x, int y,
+                                                int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+        "%5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void ex_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// acc[c] += the 32 TMEM columns at taddr + 32 c
+template <int NC>
+__device__ __forceinline__ void ex_promote(float (&acc)[NC][32], uint32_t taddr) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        uint32_t r[32];
+        tmem_ld32_issue(taddr + 32 * c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[c][e] += __uint_as_float(r[e]);
+    }
+}
+
+// One warp's share of a finished tile: 32 rows (one per lane) x 32 NC columns from column j0. Rows go out
+// through the warp's 4 KB stage, 128 bytes of columns at a time: whole 32-row groups by TMA (columns
+// past J are clipped), a group that holds the expert's last row by 16-byte stores of its valid rows only.
+//   row0: first output row of the warp; nvalid: its rows that exist (<= 0: none); z: expert (wgrad)
+template <typename TC, int NC, int OP, int KIND>
+__device__ __forceinline__ void ex_store(float (&acc)[NC][32], int row0, int nvalid, int j0, int e, const ExpertArgs& a,
+                                         const CUtensorMap* mapC, unsigned char* stage, uint32_t stage_s) {
+    constexpr int CW = 128 / (int)sizeof(TC);   // columns per 128 bytes: 32 (fp32) or 64
+    constexpr int PER = CW / 32;                // 32-column groups per 128 bytes
+    const int lane = threadIdx.x & 31;
+    if (nvalid <= 0) return;                    // uniform across the warp
+    float xs = 1.f;
+    if constexpr (KIND == EX_F8) xs = lane < nvalid ? a.x_scale[row0 + lane] : 0.f;
+#pragma unroll
+    for (int c = 0; c < NC / PER; ++c) {
+        const int n0 = j0 + c * CW;
+        if (n0 >= a.J) break;                   // uniform across the warp
+        if constexpr (OP == EX_FWD) {
+            const float* bias = a.bias ? a.bias + (long long)e * a.J : nullptr;
+            const float* wsc = KIND == EX_F8 ? a.w_scale + (long long)e * a.J : nullptr;
+#pragma unroll
+            for (int p = 0; p < PER; ++p)
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                    const int col = n0 + 32 * p + q;
+                    const bool in = col < a.J;
+                    float& v = acc[c * PER + p][q];
+                    if constexpr (KIND == EX_F8) v *= xs * (in ? __ldg(wsc + col) : 0.f);
+                    if (bias) v += in ? __ldg(bias + col) : 0.f;
+                    // not fmaxf: a NaN stays one
+                    if (a.relu) v = v < 0.f ? 0.f : v;
+                }
+        }
+        if (lane == 0) bulk_wait_read0();       // the previous chunk's store has read the stage
+        __syncwarp();
+        unsigned char* row = stage + lane * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint4 w;
+            if constexpr (sizeof(TC) == 2) {
+                union {
+                    TC t[8];
+                    uint4 w;
+                } u;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) u.t[k] = Cvt<TC>::from_f(acc[c * PER + q / 4][(q % 4) * 8 + k]);
+                w = u.w;
+            } else {
+                w = make_uint4(__float_as_uint(acc[c][4 * q]), __float_as_uint(acc[c][4 * q + 1]),
+                               __float_as_uint(acc[c][4 * q + 2]), __float_as_uint(acc[c][4 * q + 3]));
+            }
+            *reinterpret_cast<uint4*>(row + 16 * (q ^ (lane & 7))) = w;
+        }
+        if (OP == EX_WGRAD || nvalid >= 32) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (OP == EX_WGRAD) ex_store_3d(mapC, stage_s, n0, row0, e);
+                else tma_store_2d(mapC, stage_s, n0, row0);
+            }
+        } else {
+            __syncwarp();
+            constexpr int E16 = 16 / (int)sizeof(TC);
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                const int r = it * 4 + (lane >> 3), q = lane & 7;
+                const int col = n0 + q * E16;
+                if (r < nvalid && col < a.J) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + 16 * (q ^ (r & 7)));
+                    TC* dst = static_cast<TC*>(a.C) + (long long)(row0 + r) * a.ldc + col;
+                    if (col + E16 <= a.J) {
+                        *reinterpret_cast<uint4*>(dst) = w;
+                    } else {
+                        const TC* src = reinterpret_cast<const TC*>(&w);
+#pragma unroll
+                        for (int k = 0; k < E16; ++k)
+                            if (col + k < a.J) dst[k] = src[k];
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// k-blocks of a tile: the reduction length of fwd and dgrad, the expert's rows in wgrad.
+template <int OP, int KIND>
+__device__ __forceinline__ int ex_kblocks(const ExpertArgs& a, int rows) {
+    constexpr int KE = KIND == EX_F8 ? 128 : 64;
+    return ((OP == EX_WGRAD ? rows : a.R) + KE - 1) / KE;
+}
+
+template <typename TC, int OP, int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
+    expert_pair_kernel(const __grid_constant__ ExpertMaps maps, const __grid_constant__ ExpertArgs a, uint32_t id) {
+    constexpr bool AMN = OP == EX_WGRAD, BMN = OP != EX_FWD;
+    constexpr int KE = KIND == EX_F8 ? 128 : 64;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = su32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    unsigned char* gbase = smem_raw + (base - raw);
+    Ranges* rg = reinterpret_cast<Ranges*>(gbase + EX_STAGES2 * EX_STAGE2_BYTES + OUT_BYTES);
+    ExBars<EX_STAGES2>* bars = reinterpret_cast<ExBars<EX_STAGES2>*>(rg + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const int npair = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < EX_STAGES2; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->tfull[i], 1);
+            mbar_init(&bars->tempty[i], 2 * EPI_WARPS);
+        }
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&bars->tmem_base)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    pdl_wait();
+    if (warp == 2) read_ranges(a, rg, a.count && blockIdx.x == 0);
+    fence_before();
+    cluster_sync_all();
+    fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    volatile int* abort = &bars->abort;
+    bool timed_out = false;
+    TileWalk walk{rg, a.E, (a.J + 255) / 256, OP == EX_WGRAD ? 0 : 256, (a.I + 255) / 256};
+    int mb, cb;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(EX_REGS_LOW));
+        if (warp == 0) {
+            if (lane == 0) {
+                int s = 0;
+                uint32_t ph = 0;
+                for (long long t = pair; !timed_out && walk.seek(t, mb, cb); t += npair) {
+                    const int e = walk.e, r0 = rg->begin[e], rows = rg->end[e] - r0;
+                    const int nk = ex_kblocks<OP, KIND>(a, rows);
+                    const int arow = mb * 256 + (int)rank * 128, brow = cb * 256 + (int)rank * 128;
+                    for (int kb = 0; kb < nk; ++kb) {
+                        if (!mbar_wait(&bars->empty[s], ph ^ 1u, abort)) {
+                            timed_out = true;
+                            break;
+                        }
+                        const uint32_t sa = base + s * EX_STAGE2_BYTES, sb = sa + EX_STAGE2_BYTES / 2;
+                        const uint32_t bar = map_rank(su32(&bars->full[s]), 0);
+                        if (leader) mbar_expect_tx(&bars->full[s], 2 * EX_STAGE2_BYTES);
+                        if constexpr (OP == EX_WGRAD) {
+                            if (kb * KE + KE <= rows) {
+#pragma unroll
+                                for (int b = 0; b < 2; ++b) {
+                                    tma_load_2d_pair(sa + b * 8192, &maps.a, bar, arow + 64 * b, r0 + kb * KE);
+                                    tma_load_2d_pair(sb + b * 8192, &maps.b, bar, brow + 64 * b, r0 + kb * KE);
+                                }
+                            } else {
+#pragma unroll
+                                for (int b = 0; b < 2; ++b) {
+                                    ex_load_3d_pair(sa + b * 8192, &maps.at, bar, arow + 64 * b, 0, e);
+                                    ex_load_3d_pair(sb + b * 8192, &maps.bt, bar, brow + 64 * b, 0, e);
+                                }
+                            }
+                        } else {
+                            tma_load_2d_pair(sa, &maps.a, bar, kb * KE, r0 + arow);
+                            if constexpr (OP == EX_FWD) {
+                                ex_load_3d_pair(sb, &maps.b, bar, kb * KE, brow, e);
+                            } else {
+#pragma unroll
+                                for (int b = 0; b < 2; ++b)
+                                    ex_load_3d_pair(sb + b * 8192, &maps.b, bar, brow + 64 * b, kb * KE, e);
+                            }
+                        }
+                        if (++s == EX_STAGES2) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                if (timed_out) *abort = 1;
+                // every load this CTA issued completes before it may exit: the leader's MMA commits release
+                // each stage after consuming it (bounded)
+                for (int q = 0; q < EX_STAGES2; ++q) {
+                    mbar_wait(&bars->empty[s], ph ^ 1u, abort, true);
+                    if (++s == EX_STAGES2) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            if (lane == 0 && leader) {
+                int s = 0;
+                uint32_t ph = 0, part = 0;   // accumulator parts so far: part n uses TMEM buffer n & 1
+                for (long long t = pair; !timed_out && walk.seek(t, mb, cb); t += npair) {
+                    const int nk = ex_kblocks<OP, KIND>(a, rg->end[walk.e] - rg->begin[walk.e]);
+                    for (int kb = 0; kb < nk; ++kb) {
+                        const int acc = (int)(part & 1u);
+                        if ((kb % PART) == 0 && !mbar_wait(&bars->tempty[acc], ((part >> 1) & 1u) ^ 1u, abort)) {
+                            timed_out = true;
+                            break;
+                        }
+                        if (!mbar_wait(&bars->full[s], ph, abort)) {
+                            timed_out = true;
+                            break;
+                        }
+                        fence_after();
+                        const uint32_t d = tmem + (uint32_t)(acc * 256);
+                        const uint32_t sa = base + s * EX_STAGE2_BYTES, sb = sa + EX_STAGE2_BYTES / 2;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t da = AMN ? sdesc_mn16(sa + k * 2048) : sdesc(sa + k * 32);
+                            const uint64_t db = BMN ? sdesc_mn16(sb + k * 2048) : sdesc(sb + k * 32);
+                            ex_umma<KIND, 2>(d, da, db, id, ((kb % PART) | k) != 0);
+                        }
+                        umma2_commit_both(&bars->empty[s]);
+                        if ((kb % PART) == PART - 1 || kb + 1 == nk) {
+                            umma2_commit_both(&bars->tfull[acc]);
+                            ++part;
+                        }
+                        if (++s == EX_STAGES2) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                if (timed_out) *abort = 1;
+                umma2_commit_both(&bars->drain);
+                mbar_wait(&bars->drain, 0, abort, true);
+            } else if (lane == 0) {
+                mbar_wait(&bars->drain, 0, abort, true);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EX_REGS_HIGH));
+        const int ew = warp - 4, q = warp & 3, h = ew >> 2;
+        unsigned char* stage = gbase + EX_STAGES2 * EX_STAGE2_BYTES + ew * STAGE_OUT_BYTES;
+        const uint32_t stage_s = base + EX_STAGES2 * EX_STAGE2_BYTES + ew * STAGE_OUT_BYTES;
+        const uint32_t lead_tempty0 = map_rank(su32(&bars->tempty[0]), 0);
+        const uint32_t lead_tempty1 = map_rank(su32(&bars->tempty[1]), 0);
+        uint32_t part = 0;
+        for (long long t = pair; !timed_out && walk.seek(t, mb, cb); t += npair) {
+            const int e = walk.e, r0 = rg->begin[e], rows = rg->end[e] - r0;
+            const int parts = (ex_kblocks<OP, KIND>(a, rows) + PART - 1) / PART;
+            float acc[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int x = 0; x < 32; ++x) acc[c][x] = 0.f;
+            for (int p = 0; p < parts; ++p, ++part) {
+                const int b = (int)(part & 1u);
+                if (!mbar_wait(&bars->tfull[b], (part >> 1) & 1u, abort)) {
+                    timed_out = true;
+                    break;
+                }
+                fence_after();
+                ex_promote<4>(acc, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256 + h * 128));
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(b ? lead_tempty1 : lead_tempty0);
+            }
+            if (timed_out) break;
+            const int in_tile = mb * 256 + (int)rank * 128 + q * 32;
+            if constexpr (OP == EX_WGRAD)
+                ex_store<TC, 4, OP, KIND>(acc, in_tile, a.I - in_tile, cb * 256 + h * 128, e, a, &maps.c, stage, stage_s);
+            else
+                ex_store<TC, 4, OP, KIND>(acc, r0 + in_tile, rows - in_tile, cb * 256 + h * 128, e, a, &maps.c, stage,
+                                          stage_s);
+        }
+        if (timed_out) *abort = 1;
+        if (lane == 0) bulk_wait_all0();
+    }
+    if (timed_out && lane == 0) atomicOr(&a.err->flags, (unsigned)ERR_TIMEOUT);
+    fence_before();
+    cluster_sync_all();   // no CTA frees TMEM or exits while its pair still signals it
+    fence_after();
+    if (warp == 1) {
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// ------------------------------------------------------------------ one SM per tile (forward)
+
+template <int BNT>
+struct ExTile {
+    static constexpr int NS = BNT == 64 ? 8 : 6;
+    static constexpr int STAGE = (128 + BNT) * 128;
+    static constexpr int WC = BNT == 64 ? 64 : BNT / 2;     // columns per epilogue warp
+    static constexpr int TMEM = 2 * BNT;
+    static constexpr int SMEM = NS * STAGE + OUT_BYTES + (int)sizeof(Ranges) + (int)sizeof(ExBars<NS>) + 256;
+};
+
+template <typename TC, int KIND, int BNT>
+__global__ void __launch_bounds__(THREADS, 1)
+    expert_tile_kernel(const __grid_constant__ ExpertMaps maps, const __grid_constant__ ExpertArgs a, uint32_t id) {
+    using T = ExTile<BNT>;
+    constexpr int NS = T::NS;
+    constexpr int KE = KIND == EX_F8 ? 128 : 64;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = su32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    unsigned char* gbase = smem_raw + (base - raw);
+    Ranges* rg = reinterpret_cast<Ranges*>(gbase + NS * T::STAGE + OUT_BYTES);
+    ExBars<NS>* bars = reinterpret_cast<ExBars<NS>*>(rg + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nk = ex_kblocks<EX_FWD, KIND>(a, 0);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->tfull[i], 1);
+            mbar_init(&bars->tempty[i], EPI_WARPS);
+        }
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&bars->tmem_base)),
+                     "r"(T::TMEM));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_wait();
+    if (warp == 2) read_ranges(a, rg, a.count && blockIdx.x == 0);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    volatile int* abort = &bars->abort;
+    bool timed_out = false;
+    TileWalk walk{rg, a.E, (a.J + BNT - 1) / BNT, 128, 0};
+    int mb, cb;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            for (long long t = blockIdx.x; !timed_out && walk.seek(t, mb, cb); t += gridDim.x) {
+                const int e = walk.e, row = rg->begin[e] + mb * 128;
+                const bool few = rg->end[e] - row <= 32;
+                const uint32_t tx = (uint32_t)((few ? 32 : 128) + BNT) * 128u;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!mbar_wait(&bars->empty[s], ph ^ 1u, abort)) {
+                        timed_out = true;
+                        break;
+                    }
+                    const uint32_t sa = base + s * T::STAGE;
+                    mbar_expect_tx(&bars->full[s], tx);
+                    tma_load_2d(sa, few ? &maps.a32 : &maps.a, &bars->full[s], kb * KE, row);
+                    ex_load_3d(sa + 128 * 128, &maps.b, &bars->full[s], kb * KE, cb * BNT, e);
+                    if (++s == NS) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (timed_out) *abort = 1;
+            // drain, also when another role gave up: every stage whose load may still be in flight completes its
+            // full phase before the CTA may exit (a stage never loaded, or already consumed, passes at once)
+            for (int q = 0; q < NS; ++q) {
+                if (--s < 0) {
+                    s = NS - 1;
+                    ph ^= 1u;
+                }
+                mbar_wait(&bars->full[s], ph, abort, true);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, part = 0;
+            for (long long t = blockIdx.x; !timed_out && walk.seek(t, mb, cb); t += gridDim.x) {
+                for (int kb = 0; kb < nk; ++kb) {
+                    const int acc = (int)(part & 1u);
+                    if ((kb % PART) == 0 && !mbar_wait(&bars->tempty[acc], ((part >> 1) & 1u) ^ 1u, abort)) {
+                        timed_out = true;
+                        break;
+                    }
+                    if (!mbar_wait(&bars->full[s], ph, abort)) {
+                        timed_out = true;
+                        break;
+                    }
+                    fence_after();
+                    const uint32_t d = tmem + (uint32_t)(acc * BNT);
+                    const uint32_t sa = base + s * T::STAGE, sb = sa + 128 * 128;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ex_umma<KIND, 1>(d, sdesc(sa + k * 32), sdesc(sb + k * 32), id, ((kb % PART) | k) != 0);
+                    umma_commit(&bars->empty[s]);
+                    if ((kb % PART) == PART - 1 || kb + 1 == nk) {
+                        umma_commit(&bars->tfull[acc]);
+                        ++part;
+                    }
+                    if (++s == NS) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (timed_out) *abort = 1;
+            umma_commit(&bars->drain);
+            mbar_wait(&bars->drain, 0, abort, true);
+        }
+    } else {
+        constexpr int NC = T::WC / 32;
+        const int ew = warp - 2, q = warp & 3, h = ew >> 2;
+        const bool active = h * T::WC < BNT;
+        unsigned char* stage = gbase + NS * T::STAGE + ew * STAGE_OUT_BYTES;
+        const uint32_t stage_s = base + NS * T::STAGE + ew * STAGE_OUT_BYTES;
+        const int parts = (nk + PART - 1) / PART;
+        uint32_t part = 0;
+        for (long long t = blockIdx.x; !timed_out && walk.seek(t, mb, cb); t += gridDim.x) {
+            const int e = walk.e, row = rg->begin[e] + mb * 128 + q * 32;
+            const bool some = active && row < rg->end[e];
+            float acc[NC][32];
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int x = 0; x < 32; ++x) acc[c][x] = 0.f;
+            for (int p = 0; p < parts; ++p, ++part) {
+                const int b = (int)(part & 1u);
+                if (!mbar_wait(&bars->tfull[b], (part >> 1) & 1u, abort)) {
+                    timed_out = true;
+                    break;
+                }
+                fence_after();
+                if (some) ex_promote<NC>(acc, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BNT + h * T::WC));
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->tempty[b]);
+            }
+            if (timed_out) break;
+            if (some)
+                ex_store<TC, NC, EX_FWD, KIND>(acc, row, rg->end[e] - row, cb * BNT + h * T::WC, e, a, &maps.c, stage,
+                                               stage_s);
+        }
+        if (timed_out) *abort = 1;
+        if (lane == 0) bulk_wait_all0();
+    }
+    if (timed_out && lane == 0) atomicOr(&a.err->flags, (unsigned)ERR_TIMEOUT);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1) {
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(T::TMEM));
+    }
+}
+
+constexpr int EX_SMEM2 =
+    EX_STAGES2 * EX_STAGE2_BYTES + OUT_BYTES + (int)sizeof(Ranges) + (int)sizeof(ExBars<EX_STAGES2>) + 256;
+static_assert(EX_SMEM2 <= 227 * 1024 && ExTile<64>::SMEM <= 227 * 1024 && ExTile<128>::SMEM <= 227 * 1024, "shared memory");
+
+// ------------------------------------------------------------------ backward: dP, bias sums, padded last blocks
+
+struct PrepArgs {
+    ExpertArgs x;             // E, M, offsets, count, err
+    int N, K;
+    int nslices;              // column slices of dY; the slices after them are X's
+    const void* dY;
+    long long lddy;
+    const void* Y;            // ReLU: the forward's output
+    long long ldyy;
+    const void* X;
+    long long ldx;
+    void* dP;                 // ReLU: the masked gradient [M][ldp]
+    long long ldp;
+    float* part;              // bias sums: [chunk][N], or null
+    void* tail_dp;            // [E][64][ldp], or null
+    void* tail_x;             // [E][64][ldtx]
+    long long ldtx;
+};
+
+constexpr int PREP_ROWS = 64;     // rows per chunk: one reduction block of wgrad
+constexpr int PREP_COLS = 8;      // columns per thread: 16 bytes
+
+// The expert and first row of chunk number `chunk` (experts in order, each cut into 64-row chunks from its first
+// row), found by the whole block's first warp; e = E if there is no such chunk.
+__device__ __forceinline__ void find_chunk(const Ranges* rg, int E, long long chunk, int* e_out, long long* j_out) {
+    const int lane = threadIdx.x & 31;
+    long long seen = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        const long long mine = e < E ? (rg->end[e] - rg->begin[e] + PREP_ROWS - 1) / PREP_ROWS : 0;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const bool here = chunk >= seen + incl - mine && chunk < seen + incl;
+        if (here) {
+            *e_out = e;
+            *j_out = chunk - (seen + incl - mine);
+        }
+        if (__any_sync(0xffffffffu, here)) return;
+        seen += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) *e_out = E;
+}
+
+// A run of which the first `valid` columns exist: the rest reads as zeros.
+template <typename T>
+__device__ __forceinline__ void load_run(RowRaw<T, PREP_COLS>& v, const T* p, int valid) {
+    if (valid == PREP_COLS) {
+        v.load(p);
+    } else {
+        v.zero();
+#pragma unroll
+        for (int k = 0; k < PREP_COLS; ++k)
+            if (k < valid) v.e[k] = p[k];
+    }
+}
+
+// Block (chunk, slice): up to 64 rows x 256 * 8 columns, one run of 8 columns per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) expert_prep_kernel(const __grid_constant__ PrepArgs a) {
+    pdl_wait();
+    __shared__ Ranges rg;
+    __shared__ int se;
+    __shared__ long long sj;
+    if (threadIdx.x < 32) {
+        read_ranges(a.x, &rg, a.x.count && blockIdx.x == 0 && blockIdx.y == 0);
+        __syncwarp();
+        find_chunk(&rg, a.x.E, blockIdx.x, &se, &sj);
+    }
+    __syncthreads();
+    const int e = se;
+    if (e >= a.x.E) return;
+    const long long r0 = rg.begin[e] + sj * PREP_ROWS;
+    const int rows = (int)(rg.end[e] - r0 < PREP_ROWS ? rg.end[e] - r0 : PREP_ROWS);
+    const bool tail = rows < PREP_ROWS;
+    if ((int)blockIdx.y >= a.nslices) {
+        // X: only the padded copy of a last block
+        const long long c = ((long long)(blockIdx.y - a.nslices) * 256 + threadIdx.x) * PREP_COLS;
+        if (!tail || !a.tail_x || c >= a.K) return;
+        const T* x = static_cast<const T*>(a.X) + r0 * a.ldx + c;
+        T* out = static_cast<T*>(a.tail_x) + (long long)e * PREP_ROWS * a.ldtx + c;
+        const int valid = a.K - c < PREP_COLS ? (int)(a.K - c) : PREP_COLS;
+        for (int r = 0; r < PREP_ROWS; ++r) {
+            RowRaw<T, PREP_COLS> v;
+            if (r < rows) load_run(v, x + r * a.ldx, valid);
+            else v.zero();
+            v.store(out + r * a.ldtx);
+        }
+        return;
+    }
+    const long long c = ((long long)blockIdx.y * 256 + threadIdx.x) * PREP_COLS;
+    if (c >= a.N) return;
+    const bool mask = a.Y != nullptr;
+    if (!mask && !a.part && !(tail && a.tail_dp)) return;
+    const T* dy = static_cast<const T*>(a.dY) + r0 * a.lddy + c;
+    const T* y = mask ? static_cast<const T*>(a.Y) + r0 * a.ldyy + c : nullptr;
+    T* dp = mask ? static_cast<T*>(a.dP) + r0 * a.ldp + c : nullptr;
+    T* tl = tail && a.tail_dp ? static_cast<T*>(a.tail_dp) + (long long)e * PREP_ROWS * a.ldp + c : nullptr;
+    const int valid = a.N - c < PREP_COLS ? (int)(a.N - c) : PREP_COLS;
+    float sum[PREP_COLS];
+#pragma unroll
+    for (int k = 0; k < PREP_COLS; ++k) sum[k] = 0.f;
+    constexpr int U = 4;
+    for (int r = 0; r < rows; r += U) {
+        RowRaw<T, PREP_COLS> g[U], f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r + u < rows) {
+                load_run(g[u], dy + (long long)(r + u) * a.lddy, valid);
+                if (mask) load_run(f[u], y + (long long)(r + u) * a.ldyy, valid);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r + u < rows) {
+                float v[PREP_COLS];
+                g[u].get(v);
+                if (mask) {
+                    float o[PREP_COLS];
+                    f[u].get(o);
+#pragma unroll
+                    for (int k = 0; k < PREP_COLS; ++k)
+                        if (!(o[k] > 0.f)) v[k] = 0.f;
+                    g[u].set(v);
+                    g[u].store(dp + (long long)(r + u) * a.ldp);
+                }
+                if (tl) g[u].store(tl + (long long)(r + u) * a.ldp);
+#pragma unroll
+                for (int k = 0; k < PREP_COLS; ++k) sum[k] += v[k];
+            }
+    }
+    if (tl) {
+        RowRaw<T, PREP_COLS> z;
+        z.zero();
+        for (int r = rows; r < PREP_ROWS; ++r) z.store(tl + (long long)r * a.ldp);
+    }
+    if (a.part) {
+#pragma unroll
+        for (int k = 0; k < PREP_COLS; ++k)
+            if (c + k < a.N) a.part[(long long)blockIdx.x * a.N + c + k] = sum[k];
+    }
+}
+
+// db[e][n] = sum over the expert's chunks, in order.
+__global__ void __launch_bounds__(256) expert_bias_kernel(const __grid_constant__ ExpertArgs a, int N,
+                                                          const float* __restrict__ part, float* __restrict__ db) {
+    pdl_wait();
+    __shared__ Ranges rg;
+    __shared__ long long first;
+    const int e = blockIdx.y;
+    if (threadIdx.x < 32) {
+        read_ranges(a, &rg, false);
+        __syncwarp();
+        long long s = 0;
+        for (int q = threadIdx.x; q < e; q += 32) s += (rg.end[q] - rg.begin[q] + PREP_ROWS - 1) / PREP_ROWS;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) first = s;
+    }
+    __syncthreads();
+    const int n = blockIdx.x * blockDim.x + threadIdx.x;
+    if (n >= N) return;
+    const int chunks = (rg.end[e] - rg.begin[e] + PREP_ROWS - 1) / PREP_ROWS;
+    const float* p = part + first * N + n;
+    float s = 0.f;
+#pragma unroll 8
+    for (int j = 0; j < chunks; ++j) s += p[(long long)j * N];
+    db[(long long)e * N + n] = s;
+}
+
+// ------------------------------------------------------------------ host side
+
+namespace {
+
+bool ex_map(CUtensorMap* m, const void* p, int es, dlrm_dtype dt, int rank, long long inner, long long mid, long long outer,
+            long long ld, int box_inner, int box_mid) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)mid, (cuuint64_t)outer};
+    const cuuint64_t strides[2] = {(cuuint64_t)(ld * es), (cuuint64_t)(mid * ld * es)};
+    const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_mid, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapDataType t = dt == DLRM_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : dt == DLRM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                  : dt == DLRM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return enc(m, t, rank, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int ex_size(dlrm_dtype dt) { return dt == DLRM_F32 ? 4 : dt == DLRM_E4M3 ? 1 : 2; }
+
+template <typename TC, int OP, int KIND>
+dlrm_status launch_pair(const ExpertMaps& maps, const ExpertArgs& a, uint32_t id, long long tiles, cudaStream_t st) {
+    auto kern = expert_pair_kernel<TC, OP, KIND>;
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, EX_SMEM2);
+    const int pairs = device_sms() / 2;
+    const dim3 grid((unsigned)(2 * std::min<long long>(tiles, pairs)));
+    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(EX_THREADS2), (size_t)EX_SMEM2, st, maps, a, id));
+    return DLRM_OK;
+}
+
+template <typename TC, int KIND, int BNT>
+dlrm_status launch_tile(const ExpertMaps& maps, const ExpertArgs& a, uint32_t id, long long tiles, cudaStream_t st) {
+    auto kern = expert_tile_kernel<TC, KIND, BNT>;
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ExTile<BNT>::SMEM);
+    const dim3 grid((unsigned)std::min<long long>(tiles, device_sms()));
+    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(THREADS), (size_t)ExTile<BNT>::SMEM, st, maps, a, id));
+    return DLRM_OK;
+}
+
+// Most tiles a call can have: row blocks of every expert, the experts with rows being at most min(E, M).
+long long most_tiles(int E, long long M, int rows_per, long long nb) {
+    return (M / rows_per + std::min<long long>(E, M)) * nb;
+}
+
+}  // namespace
+}  // namespace tc
+
+dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offsets, const void* X, long long ldx,
+                               const float* x_scale, dlrm_dtype dt, const void* W, long long ldw, const float* w_scale,
+                               const float* bias, bool relu, void* Y, long long ldy, dlrm_dtype y_dt, ErrRecord* err,
+                               cudaStream_t st) {
+    using namespace tc;
+    const int es = ex_size(dt), ke = 128 / es;
+    ExpertArgs a{E, M, N, 0, K, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, err};
+    // SM pairs once their 256 x 256 tiles can fill them (rows spread evenly over the experts); otherwise one SM
+    // per tile, 128 columns wide, or 64 when that leaves SMs without a tile
+    const long long nb2 = (N + 255) / 256;
+    const bool pair = ((long long)M / 256) * nb2 >= device_sms() / 2;
+    const long long rb = (M + 127) / 128 > std::min(E, M) ? (M + 127) / 128 : std::min(E, M);
+    const int bnt = rb * ((N + 127) / 128) >= device_sms() ? 128 : 64;
+    ExpertMaps maps{};
+    if (!ex_map(&maps.a, X, es, dt, 2, K, M, 1, ldx, ke, 128) || !ex_map(&maps.a32, X, es, dt, 2, K, M, 1, ldx, ke, 32) ||
+        !ex_map(&maps.b, W, es, dt, 3, K, N, E, ldw, ke, pair ? 128 : bnt) ||
+        !ex_map(&maps.c, Y, ex_size(y_dt), y_dt, 2, N, M, 1, ldy, 128 / ex_size(y_dt), 32))
+        return DLRM_ERR_CUDA;
+    const int fmt = dt == DLRM_BF16 ? 1 : 0;
+#define DLRM_EX_FWD(TC, KIND)                                                                                           \
+    return pair ? launch_pair<TC, EX_FWD, KIND>(maps, a, ex_idesc(fmt, false, false, 256, 256), most_tiles(E, M, 256, nb2), st) \
+           : bnt == 128                                                                                                 \
+               ? launch_tile<TC, KIND, 128>(maps, a, ex_idesc(fmt, false, false, 128, 128),                             \
+                                            most_tiles(E, M, 128, (N + 127) / 128), st)                                 \
+               : launch_tile<TC, KIND, 64>(maps, a, ex_idesc(fmt, false, false, 128, 64),                               \
+                                           most_tiles(E, M, 128, (N + 63) / 64), st);
+    if (dt == DLRM_E4M3) {
+        if (y_dt == DLRM_F32) DLRM_EX_FWD(float, EX_F8)
+        if (y_dt == DLRM_BF16) DLRM_EX_FWD(__nv_bfloat16, EX_F8)
+        DLRM_EX_FWD(__half, EX_F8)
+    }
+    if (y_dt == DLRM_F32) DLRM_EX_FWD(float, EX_F16)
+    if (y_dt == DLRM_BF16) DLRM_EX_FWD(__nv_bfloat16, EX_F16)
+    DLRM_EX_FWD(__half, EX_F16)
+#undef DLRM_EX_FWD
+}
+
+ExpertsLayout experts_layout(int E, long long M, int N, int K, bool relu) {
+    ExpertsLayout L;
+    size_t off = align_up(DLRM_ERR_RECORD_BYTES, 256);
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = align_up(off + bytes, 256);
+        return o;
+    };
+    L.ldp = (N + 7) / 8 * 8;
+    L.ldtx = (K + 7) / 8 * 8;
+    L.dp = take(relu ? (size_t)2 * M * L.ldp : 0);
+    L.tail_dp = take((size_t)2 * E * tc::PREP_ROWS * L.ldp);
+    L.tail_x = take((size_t)2 * E * tc::PREP_ROWS * L.ldtx);
+    L.part = take(sizeof(float) * (size_t)(M / tc::PREP_ROWS + E) * N);
+    L.total = off;
+    return L;
+}
+
+dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offsets, const void* dY, long long lddy,
+                               const void* Y, long long ldyy, const void* X, long long ldx, const void* W, long long ldw,
+                               dlrm_dtype dt, void* dX, long long lddx, dlrm_dtype dx_dt, void* dW, long long lddw,
+                               dlrm_dtype dw_dt, float* db, char* ws, cudaStream_t st) {
+    using namespace tc;
+    const bool relu = Y != nullptr;
+    const ExpertsLayout L = experts_layout(E, M, N, K, relu);
+    ErrRecord* err = reinterpret_cast<ErrRecord*>(ws);
+    ExpertArgs base{E, M, 0, 0, 0, offsets, true, nullptr, nullptr, nullptr, false, nullptr, 0, err};
+    float* part = reinterpret_cast<float*>(ws + L.part);
+    const void* dP = relu ? (const void*)(ws + L.dp) : dY;
+    const long long ldp = relu ? L.ldp : lddy;
+    if (M > 0 && (relu || db || dW)) {
+        PrepArgs p{};
+        p.x = base;
+        p.N = N;
+        p.K = K;
+        const int per = 256 * PREP_COLS;
+        p.nslices = (N + per - 1) / per;
+        const int xs = dW ? (K + per - 1) / per : 0;
+        p.dY = dY;
+        p.lddy = lddy;
+        p.Y = Y;
+        p.ldyy = ldyy;
+        p.X = X;
+        p.ldx = ldx;
+        p.dP = ws + L.dp;
+        p.ldp = L.ldp;
+        p.part = db ? part : nullptr;
+        p.tail_dp = dW ? ws + L.tail_dp : nullptr;
+        p.tail_x = dW ? ws + L.tail_x : nullptr;
+        p.ldtx = L.ldtx;
+        const dim3 grid((unsigned)(M / PREP_ROWS + std::min(E, M)), p.nslices + xs);
+        if (dt == DLRM_BF16) DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, p));
+        else DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__half>, grid, dim3(256), 0, st, p));
+        base.count = false;
+    }
+    if (db) {
+        DLRM_PDL_CHECK(launch_pdl(expert_bias_kernel, dim3((N + 255) / 256, E), dim3(256), 0, st, base, N,
+                                  (const float*)part, db));
+    }
+    const int fmt = dt == DLRM_BF16 ? 1 : 0;
+    if (dX && M > 0) {
+        ExpertArgs a = base;
+        a.J = K;
+        a.R = N;
+        a.C = dX;
+        a.ldc = lddx;
+        ExpertMaps maps{};
+        if (!ex_map(&maps.a, dP, 2, dt, 2, N, M, 1, ldp, 64, 128) || !ex_map(&maps.b, W, 2, dt, 3, K, N, E, ldw, 64, 64) ||
+            !ex_map(&maps.c, dX, ex_size(dx_dt), dx_dt, 2, K, M, 1, lddx, 128 / ex_size(dx_dt), 32))
+            return DLRM_ERR_CUDA;
+        const long long tiles = most_tiles(E, M, 256, (K + 255) / 256);
+        const uint32_t id = ex_idesc(fmt, false, true, 256, 256);
+        const dlrm_status r = dx_dt == DLRM_F32    ? launch_pair<float, EX_DGRAD, EX_F16>(maps, a, id, tiles, st)
+                              : dx_dt == DLRM_BF16 ? launch_pair<__nv_bfloat16, EX_DGRAD, EX_F16>(maps, a, id, tiles, st)
+                                                   : launch_pair<__half, EX_DGRAD, EX_F16>(maps, a, id, tiles, st);
+        if (r != DLRM_OK) return r;
+        base.count = false;
+    }
+    if (dW) {
+        ExpertArgs a = base;
+        a.I = N;
+        a.J = K;
+        a.C = dW;
+        a.ldc = lddw;
+        ExpertMaps maps{};
+        // without rows nothing is loaded; the maps still need an address
+        const void* pa = M > 0 ? dP : ws + L.tail_dp;
+        const void* pb = M > 0 ? X : ws + L.tail_x;
+        const long long rows = M > 0 ? M : 1;
+        if (!ex_map(&maps.a, pa, 2, dt, 2, N, rows, 1, M > 0 ? ldp : L.ldp, 64, 64) ||
+            !ex_map(&maps.b, pb, 2, dt, 2, K, rows, 1, M > 0 ? ldx : L.ldtx, 64, 64) ||
+            !ex_map(&maps.at, ws + L.tail_dp, 2, dt, 3, N, PREP_ROWS, E, L.ldp, 64, 64) ||
+            !ex_map(&maps.bt, ws + L.tail_x, 2, dt, 3, K, PREP_ROWS, E, L.ldtx, 64, 64) ||
+            !ex_map(&maps.c, dW, ex_size(dw_dt), dw_dt, 3, K, N, E, lddw, 128 / ex_size(dw_dt), 32))
+            return DLRM_ERR_CUDA;
+        const long long tiles = (long long)E * ((N + 255) / 256) * ((K + 255) / 256);
+        const uint32_t id = ex_idesc(fmt, true, true, 256, 256);
+        const dlrm_status r = dw_dt == DLRM_F32    ? launch_pair<float, EX_WGRAD, EX_F16>(maps, a, id, tiles, st)
+                              : dw_dt == DLRM_BF16 ? launch_pair<__nv_bfloat16, EX_WGRAD, EX_F16>(maps, a, id, tiles, st)
+                                                   : launch_pair<__half, EX_WGRAD, EX_F16>(maps, a, id, tiles, st);
+        if (r != DLRM_OK) return r;
+    }
+    return DLRM_OK;
+}
+
+bool experts_supported() { return tc::encode_fn() != nullptr; }
+
+}  // namespace dlrm

@@ -182,6 +182,40 @@ dlrm_status launch_sparse_apply(int d, const char* base, const SparseLayout& L, 
                                 float lr, float* table, float* grad_out, uint32_t* rows_out, int32_t* n_rows_out,
                                 cudaStream_t st);
 dlrm_status launch_sgd(long long n, float lr, float* w, const float* g, cudaStream_t st);
+
+// ---- token blocks: unpooled lookups (lookup.cu), dropout.cu, norm.cu, products grouped by expert (experts.cu)
+dlrm_status launch_lookup(const void* table, dlrm_dtype dt, long long rows, int d, long long n, const int32_t* idx,
+                          float scale, void* out, long long ldo, dlrm_dtype out_dt, ErrRecord* err, cudaStream_t st);
+size_t lookup_grad_workspace(long long m, int d, long long n);
+dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* idx, float scale, const void* dout,
+                               long long ldd, dlrm_dtype dt, void* dT, dlrm_dtype dT_dt, char* ws, cudaStream_t st);
+dlrm_status launch_dropout(long long n, const void* x, const void* residual, dlrm_dtype dt, double p,
+                           const int64_t* rng, void* y, cudaStream_t st);
+// y_scale non-null: y holds e4m3 codes
+dlrm_status launch_rmsnorm_fwd(int rows, int d, const void* x, long long ldx, const void* res, long long ldres,
+                               const float* w, float eps, dlrm_dtype dt, void* h, long long ldh, void* y,
+                               long long ldy, float* y_scale, float* rstd, cudaStream_t st);
+size_t rmsnorm_bwd_partial_floats(int rows, int d);
+dlrm_status launch_rmsnorm_bwd(int rows, int d, const void* dy, long long lddy, const void* h, long long ldh,
+                               const float* rstd, const float* w, const void* dh, long long lddh, dlrm_dtype dt,
+                               void* dx, long long lddx, float* dw, float* partial, cudaStream_t st);
+bool experts_supported();   // whether the driver encodes tensor maps
+dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offsets, const void* X, long long ldx,
+                               const float* x_scale, dlrm_dtype dt, const void* W, long long ldw, const float* w_scale,
+                               const float* bias, bool relu, void* Y, long long ldy, dlrm_dtype y_dt, ErrRecord* err,
+                               cudaStream_t st);
+// Byte offsets in the workspace of the experts' backward pass; row pitches in elements.
+struct ExpertsLayout {
+    long long ldp, ldtx;
+    size_t dp, tail_dp, tail_x, part, total;
+};
+ExpertsLayout experts_layout(int E, long long M, int N, int K, bool relu);
+// Y non-null: ReLU, the gradient passes where Y > 0
+dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offsets, const void* dY, long long lddy,
+                               const void* Y, long long ldyy, const void* X, long long ldx, const void* W, long long ldw,
+                               dlrm_dtype dt, void* dX, long long lddx, dlrm_dtype dx_dt, void* dW, long long lddw,
+                               dlrm_dtype dw_dt, float* db, char* ws, cudaStream_t st);
+
 size_t train_workspace_size(const dlrm_tables* T, const dlrm_mlp* bot, const dlrm_mlp* top, int B);
 // Test hook behind dlrm_set_wait_polls: the first-wait bound of each file's kernels on the current device.
 cudaError_t set_wait_polls_gemm_tc(long long polls);

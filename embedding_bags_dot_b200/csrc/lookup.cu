@@ -1,0 +1,635 @@
+// Unpooled lookups with scaling, and their gradient by sorted ids.
+//
+//   forward    out[i] = scale * T[idx_i]          (zeros for an index outside the table, which is counted)
+//   backward   dT[r]  = scale * sum_{i : idx_i = r} dout[i], in order of i, for every row r of the table
+//
+// Forward: bound by memory (n rows read, n written). Each thread moves runs of
+// up to 16 bytes of several rows, so that several row reads are in flight.
+//
+// Backward: n rows of dout read once, m rows of the table's gradient written
+// once; no atomics on values, so the result does not depend on timing.
+//   1. (id, position) pairs are sorted by id, stably: one block's bitonic
+//      sort in shared memory for short calls, else an LSD radix sort whose
+//      digits are as wide as the table needs (two passes up to 2^20 rows).
+//   2. The sorted pairs are cut into windows of fixed length, each summed by
+//      one group of threads per column slice, whatever rows they belong to, so
+//      a row looked up thousands of times costs no more per lookup than any
+//      other. A run of equal ids inside a window is final and goes straight to
+//      its row; the parts of a run that crosses windows go to a partial
+//      buffer. The same launch writes zeros to the rows nothing looked up.
+//   3. The partial sums of the crossing runs are added in window order.
+#include <algorithm>
+
+#include "kernels.cuh"
+#include "rowvec.cuh"
+
+namespace dlrm {
+namespace {
+
+// ------------------------------------------------------------------ forward
+
+struct LookupArgs {
+    long long n;
+    int d;
+    long long rows;        // of the table
+    const void* table;     // its first row
+    const int32_t* idx;
+    float scale;
+    void* out;
+    long long ldo;
+    ErrRecord* err;
+};
+
+// blockDim = (TX, 256 / TX): TX threads along a row, each on run tx, tx + TX, ...; R rows at once per thread.
+template <typename TI, typename TO, int VEC, int R>
+__global__ void __launch_bounds__(256) lookup_kernel(const __grid_constant__ LookupArgs a) {
+    pdl_wait();
+    const TI* table = static_cast<const TI*>(a.table);
+    TO* out = static_cast<TO*>(a.out);
+    const int runs = a.d / VEC;
+    for (long long i0 = ((long long)blockIdx.x * blockDim.y + threadIdx.y) * R; i0 < a.n;
+         i0 += (long long)gridDim.x * blockDim.y * R) {
+        long long row[R];
+        unsigned bad = 0;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            row[u] = -1;
+            if (i0 + u < a.n) {
+                const int v = a.idx[i0 + u];
+                if (v >= 0 && v < a.rows) row[u] = v;
+                else ++bad;
+            }
+        }
+        if (bad && threadIdx.x == 0) report(a.err, bad, 0);
+        for (int c = threadIdx.x; c < runs; c += blockDim.x) {
+            RowRaw<TI, VEC> in[R];
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                if (row[u] >= 0) in[u].load(table + row[u] * a.d + (long long)c * VEC);
+                else in[u].zero();
+            }
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                if (i0 + u >= a.n) break;
+                float v[VEC];
+                in[u].get(v);
+                // a skipped row is zero also under an infinite scale
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) v[e] = row[u] >= 0 ? v[e] * a.scale : 0.f;
+                RowRaw<TO, VEC> o;
+                o.set(v);
+                o.store(out + (i0 + u) * a.ldo + (long long)c * VEC);
+            }
+        }
+    }
+}
+
+int pow2_at_least(int n, int most) {
+    int p = 1;
+    while (p < n && p < most) p <<= 1;
+    return p;
+}
+
+template <typename TI, typename TO, int VEC>
+dlrm_status lookup_vec(const LookupArgs& a, cudaStream_t st) {
+    const int tx = pow2_at_least(a.d / VEC, 256);
+    const dim3 block(tx, 256 / tx);
+    // four rows per thread once that still gives every SM several blocks
+    const bool many = a.n / (4ll * block.y) >= 2ll * device_sms();
+    const long long per = (long long)block.y * (many ? 4 : 1);
+    const dim3 grid((unsigned)std::min<long long>((a.n + per - 1) / per, 1ll << 30));
+    if (many) DLRM_PDL_CHECK(launch_pdl(lookup_kernel<TI, TO, VEC, 4>, grid, block, 0, st, a));
+    else DLRM_PDL_CHECK(launch_pdl(lookup_kernel<TI, TO, VEC, 1>, grid, block, 0, st, a));
+    return DLRM_OK;
+}
+
+template <typename TI, typename TO>
+dlrm_status lookup_to(const LookupArgs& a, cudaStream_t st) {
+    // runs of 16 bytes of the narrower type where every row allows it, else of 4 bytes, else single elements
+    constexpr int W = 16 / (int)(sizeof(TI) < sizeof(TO) ? sizeof(TI) : sizeof(TO));
+    auto fits = [&](int vec) {
+        const int bi = std::min(16, vec * (int)sizeof(TI)), bo = std::min(16, vec * (int)sizeof(TO));
+        return a.d % vec == 0 && rows_on(a.table, (long long)a.d * sizeof(TI), bi) &&
+               rows_on(a.out, a.ldo * (long long)sizeof(TO), bo);
+    };
+    if (fits(W)) return lookup_vec<TI, TO, W>(a, st);
+    if (fits(2)) return lookup_vec<TI, TO, 2>(a, st);
+    return lookup_vec<TI, TO, 1>(a, st);
+}
+
+template <typename TI>
+dlrm_status lookup_ti(const LookupArgs& a, dlrm_dtype out_dt, cudaStream_t st) {
+    if (out_dt == DLRM_F32) return lookup_to<TI, float>(a, st);
+    if (out_dt == DLRM_F16) return lookup_to<TI, __half>(a, st);
+    return lookup_to<TI, __nv_bfloat16>(a, st);
+}
+
+// ------------------------------------------------------------------ sort of (id, position)
+
+constexpr int SORT1_MAX = 4096;        // pairs the one-block sort takes
+constexpr int DIG_BITS_MAX = 10;
+constexpr int RS_THREADS = 256;
+constexpr int RS_ITEMS = 8;            // keys per thread and tile
+constexpr int RS_TILE = RS_THREADS * RS_ITEMS;
+constexpr int RS_BLOCKS_MAX = 296;
+
+// The whole sort in one block: bitonic over 64-bit words (id, position), which are all different, so the
+// order is that of a stable sort by id. Indices outside the table get id m and end up last.
+__global__ void __launch_bounds__(1024) sort_one_block_kernel(int n, int padded, long long m,
+                                                              const int32_t* __restrict__ idx,
+                                                              uint32_t* __restrict__ keys,
+                                                              uint32_t* __restrict__ vals, ErrRecord* err) {
+    pdl_wait();
+    extern __shared__ unsigned long long pairs[];
+    unsigned bad = 0;
+    for (int i = threadIdx.x; i < padded; i += blockDim.x) {
+        unsigned long long p = ~0ull;
+        if (i < n) {
+            const int v = idx[i];
+            const bool ok = v >= 0 && v < m;
+            bad += !ok;
+            p = ((unsigned long long)(ok ? (uint32_t)v : (uint32_t)m) << 32) | (uint32_t)i;
+        }
+        pairs[i] = p;
+    }
+    report_warp(err, bad, 0);
+    for (int size = 2; size <= padded; size <<= 1) {
+        for (int step = size >> 1; step; step >>= 1) {
+            __syncthreads();
+            for (int t = threadIdx.x; t < padded / 2; t += blockDim.x) {
+                const int lo = ((t & ~(step - 1)) << 1) | (t & (step - 1)), hi = lo | step;
+                const unsigned long long x = pairs[lo], y = pairs[hi];
+                if ((x > y) == ((lo & size) == 0)) {
+                    pairs[lo] = y;
+                    pairs[hi] = x;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        keys[i] = (uint32_t)(pairs[i] >> 32);
+        vals[i] = (uint32_t)pairs[i];
+    }
+}
+
+// Radix pass: block b owns keys [b * chunk, (b + 1) * chunk). FIRST reads the indices themselves.
+template <bool FIRST>
+__device__ __forceinline__ uint32_t pass_key(const void* in, long long i, long long m) {
+    if constexpr (FIRST) {
+        const int v = static_cast<const int32_t*>(in)[i];
+        return v >= 0 && v < m ? (uint32_t)v : (uint32_t)m;
+    } else {
+        return static_cast<const uint32_t*>(in)[i];
+    }
+}
+
+// hist[b][digit] = keys of block b with that digit
+template <bool FIRST>
+__global__ void __launch_bounds__(RS_THREADS) rs_hist_kernel(long long n, long long m, const void* __restrict__ in,
+                                                             int shift, int bits, long long chunk,
+                                                             int* __restrict__ hist, ErrRecord* err) {
+    pdl_wait();
+    __shared__ int h[1 << DIG_BITS_MAX];
+    const int radix = 1 << bits;
+    for (int i = threadIdx.x; i < radix; i += blockDim.x) h[i] = 0;
+    __syncthreads();
+    const long long b0 = (long long)blockIdx.x * chunk, b1 = b0 + chunk < n ? b0 + chunk : n;
+    unsigned bad = 0;
+    for (long long i = b0 + threadIdx.x; i < b1; i += blockDim.x) {
+        const uint32_t k = pass_key<FIRST>(in, i, m);
+        if (FIRST) bad += k == (uint32_t)m;
+        atomicAdd(&h[(k >> shift) & (radix - 1)], 1);
+    }
+    if (FIRST) {
+        __syncwarp();
+        report_warp(err, bad, 0);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < radix; i += blockDim.x) hist[(long long)blockIdx.x * radix + i] = h[i];
+}
+
+// Stable scatter of block b's keys. Its first position for a digit is the count of smaller digits in all
+// blocks plus that of the same digit in earlier blocks, summed here from the histograms (at most 296 of them).
+template <bool FIRST>
+__global__ void __launch_bounds__(RS_THREADS) rs_scatter_kernel(long long n, long long m, const void* __restrict__ in,
+                                                                const uint32_t* __restrict__ vin, int shift, int bits,
+                                                                long long chunk, const int* __restrict__ hist,
+                                                                uint32_t* __restrict__ kout,
+                                                                uint32_t* __restrict__ vout) {
+    pdl_wait();
+    constexpr int W = RS_THREADS / 32;
+    constexpr int RMAX = 1 << DIG_BITS_MAX;
+    constexpr int PER = RMAX / RS_THREADS;     // digits per thread: consecutive
+    __shared__ int next[RMAX];                 // the block's next output position per digit
+    __shared__ __align__(16) unsigned short wcount[W][RMAX]; // keys of a digit met so far by each warp in this tile
+    __shared__ int wsum[W];
+    const int radix = 1 << bits;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // totals and prefixes over blocks, coalesced over digits
+    for (int dg = threadIdx.x; dg < radix; dg += RS_THREADS) {
+        int before = 0, all = 0;
+#pragma unroll 8
+        for (int b = 0; b < (int)gridDim.x; ++b) {
+            const int v = hist[(long long)b * radix + dg];
+            all += v;
+            if (b < (int)blockIdx.x) before += v;
+        }
+        next[dg] = all;
+        // kept aside until the scan over digits is known
+        reinterpret_cast<int*>(wcount)[dg] = before;
+    }
+    for (int dg = radix + threadIdx.x; dg < RMAX; dg += RS_THREADS) next[dg] = 0;
+    __syncthreads();
+    {
+        int v[PER], s = 0;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            v[e] = next[threadIdx.x * PER + e];
+            s += v[e];
+        }
+        int incl = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        int base = incl - s;
+        for (int q = 0; q < warp; ++q) base += wsum[q];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int dg = threadIdx.x * PER + e;
+            if (dg < radix) next[dg] = base + reinterpret_cast<int*>(wcount)[dg];
+            base += v[e];
+        }
+    }
+    __syncthreads();
+    const long long b0 = (long long)blockIdx.x * chunk, b1 = b0 + chunk < n ? b0 + chunk : n;
+    const unsigned lt = (1u << lane) - 1u;
+    for (long long t0 = b0; t0 < b1; t0 += RS_TILE) {
+        for (int i = threadIdx.x; i < W * RMAX / 2; i += RS_THREADS) reinterpret_cast<uint32_t*>(wcount)[i] = 0;
+        __syncthreads();
+        // warp w takes the tile's keys [w, w + 1) * 32 * RS_ITEMS, 32 at a time in order
+        const long long w0 = t0 + (long long)warp * (32 * RS_ITEMS);
+        uint32_t key[RS_ITEMS], val[RS_ITEMS];
+        int rank[RS_ITEMS];
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e) {
+            const long long i = w0 + e * 32 + lane;
+            const bool valid = i < b1;
+            key[e] = valid ? pass_key<FIRST>(in, i, m) : 0u;
+            val[e] = valid ? (FIRST ? (uint32_t)i : vin[i]) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e) {
+            const bool valid = w0 + e * 32 + lane < b1;
+            const int dg = valid ? (int)((key[e] >> shift) & (radix - 1)) : radix;   // radix: no digit
+            const unsigned peers = __match_any_sync(0xffffffffu, dg);
+            const int ahead = __popc(peers & lt);
+            const int cnt = valid ? wcount[warp][dg] : 0;
+            rank[e] = valid ? cnt + ahead : -1;
+            __syncwarp();
+            if (valid && ahead == 0) wcount[warp][dg] = (unsigned short)(cnt + __popc(peers));
+            __syncwarp();
+        }
+        __syncthreads();
+        // counts -> positions within the block's run of that digit, by warp; next moves on by the tile's total
+        for (int dg = threadIdx.x; dg < radix; dg += RS_THREADS) {
+            int run = 0;
+#pragma unroll
+            for (int q = 0; q < W; ++q) {
+                const int c = wcount[q][dg];
+                wcount[q][dg] = (unsigned short)run;
+                run += c;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e) {
+            if (rank[e] >= 0) {
+                const int dg = (int)((key[e] >> shift) & (radix - 1));
+                const long long pos = (long long)next[dg] + wcount[warp][dg] + rank[e];
+                kout[pos] = key[e];
+                vout[pos] = val[e];
+                rank[e] += wcount[warp][dg];
+            }
+        }
+        __syncthreads();
+        // next position after the tile: one past the largest rank of each digit
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e)
+            if (rank[e] >= 0) atomicAdd(&next[(key[e] >> shift) & (radix - 1)], 1);
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ sums over runs of equal ids
+
+struct SumArgs {
+    long long n, m;
+    int d;
+    long long windows;
+    int P;                    // sorted pairs per window
+    int wblocks;              // blocks of this launch that take windows; the others write zero rows
+    int slices;               // column slices
+    const uint32_t* keys;
+    const uint32_t* vals;
+    const void* dout;
+    long long ldd;
+    float scale;
+    float* partial;           // [windows][2][d]: the run entering from before, the run leaving into the next
+    void* dT;
+};
+
+// First sorted position with key >= k, by the whole warp: 32 probes at a time.
+__device__ __forceinline__ long long warp_lower_bound(const uint32_t* keys, long long n, long long k, int lane) {
+    long long lo = 0, hi = n;      // the answer is in [lo, hi]
+    while (hi - lo > 0) {
+        const long long step = (hi - lo + 31) / 32;
+        const long long at = lo + step * (lane + 1) - 1;     // last element of the lane's piece
+        const bool less = at < hi && (long long)keys[at] < k;
+        const int pieces = __popc(__ballot_sync(0xffffffffu, less));   // pieces wholly below k (sorted keys)
+        lo += step * pieces;
+        if (lo > hi) lo = hi;
+        if (step == 1) break;
+        hi = lo + step - 1 < hi ? lo + step - 1 : hi;
+    }
+    return lo;
+}
+
+// blockDim = (TX, 128 / TX): TX threads along the column slice, one window per threadIdx.y.
+template <typename TI, typename TO, int VEC>
+__global__ void __launch_bounds__(128) run_sum_kernel(const __grid_constant__ SumArgs a) {
+    pdl_wait();
+    TO* dT = static_cast<TO*>(a.dT);
+    if ((int)blockIdx.x >= a.wblocks) {
+        // zero rows: each warp takes 32 consecutive rows and finds which of them have no pair
+        const int tid = threadIdx.y * blockDim.x + threadIdx.x, lane = tid & 31;
+        const long long nw = (long long)(gridDim.x - a.wblocks) * 4;
+        for (long long g = (long long)(blockIdx.x - a.wblocks) * 4 + (tid >> 5); g * 32 < a.m; g += nw) {
+            const long long r0 = g * 32;
+            const long long lo = warp_lower_bound(a.keys, a.n, r0, lane);
+            const long long hi = lo + warp_lower_bound(a.keys + lo, a.n - lo, r0 + 32, lane);
+            // lane l: is row r0 + l among keys[lo, hi)?
+            long long x = lo, y = hi;
+            const long long mine = r0 + lane;
+            while (x < y) {
+                const long long mid = (x + y) >> 1;
+                if ((long long)a.keys[mid] < mine) x = mid + 1;
+                else y = mid;
+            }
+            const bool there = x < hi && (long long)a.keys[x] == mine;
+            unsigned empty = __ballot_sync(0xffffffffu, !there && mine < a.m);
+            RowRaw<TO, VEC> z;
+            z.zero();
+            while (empty) {
+                const int l = __ffs(empty) - 1;
+                empty &= empty - 1;
+                TO* p = dT + (r0 + l) * a.d;
+                for (int c = lane * VEC; c < a.d; c += 32 * VEC) z.store(p + c);
+            }
+        }
+        return;
+    }
+    const long long wb = blockIdx.x / a.slices;
+    const int slice = (int)(blockIdx.x - wb * a.slices);
+    const long long w = wb * blockDim.y + threadIdx.y;
+    const int c = (slice * blockDim.x + threadIdx.x) * VEC;
+    if (w >= a.windows || c >= a.d) return;
+    const long long i0 = w * a.P, i1 = i0 + a.P < a.n ? i0 + a.P : a.n;
+    const TI* dout = static_cast<const TI*>(a.dout) + c;
+    const uint32_t m = (uint32_t)a.m;
+    // the first run of the window is a continuation when the pair before it has the same id
+    bool entering = i0 > 0 && a.keys[i0 - 1] == a.keys[i0];
+    float acc[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+    constexpr int U = 8;
+    for (long long i = i0; i < i1; i += U) {
+        uint32_t key[U + 1];
+        RowRaw<TI, VEC> in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            key[u] = m;
+            if (i + u < i1) {
+                key[u] = a.keys[i + u];
+                if (key[u] != m) in[u].load(dout + (long long)a.vals[i + u] * a.ldd);
+            }
+        }
+        // the key after this group decides whether its last run ends here (m + 1: nothing follows)
+        key[U] = i + U < a.n ? a.keys[i + U] : m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= i1 || key[u] == m) break;
+            float v[VEC];
+            in[u].get(v);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[e] += v[e];
+            const bool last_here = i + u + 1 == i1;          // the window's last pair
+            const uint32_t after = last_here ? (i1 < a.n ? a.keys[i1] : m) : key[u + 1];
+            const bool ends = after != key[u];
+            if (!ends && !last_here) continue;
+            if (entering || !ends) {
+                // part of a run that crosses windows
+                float* p = a.partial + (w * 2 + (entering ? 0 : 1)) * a.d + c;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) p[e] = acc[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[e] *= a.scale;
+                RowRaw<TO, VEC> o;
+                o.set(acc);
+                o.store(dT + (long long)key[u] * a.d + c);
+            }
+            entering = false;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+        }
+    }
+}
+
+// A run that starts inside window w and goes on into w + 1: its parts are partial[w][1], partial[w + 1][0],
+// ... up to the window where it ends. blockDim = (32, 8): 32 columns, eight contiguous shares of the
+// windows, added in order.
+template <typename TO>
+__global__ void __launch_bounds__(256) run_join_kernel(const __grid_constant__ SumArgs a) {
+    pdl_wait();
+    __shared__ float part[8][33];
+    __shared__ long long last_s;
+    const long long w = blockIdx.x;
+    const long long i1 = (w + 1) * a.P;
+    if (i1 >= a.n) return;
+    const uint32_t key = a.keys[i1 - 1];
+    if (key != a.keys[i1] || key == (uint32_t)a.m) return;                    // nothing leaves this window
+    const long long i0 = w * a.P;
+    if (a.keys[i0] == key && i0 > 0 && a.keys[i0 - 1] == key) return;          // it started earlier
+    if (threadIdx.y == 0) {
+        const long long end = i1 + warp_lower_bound(a.keys + i1, a.n - i1, (long long)key + 1, threadIdx.x);
+        if (threadIdx.x == 0) last_s = (end - 1) / a.P;
+    }
+    __syncthreads();
+    const long long cnt = last_s - w;            // windows after w that hold a part
+    const long long per = (cnt + 7) / 8;
+    const long long j0 = 1 + threadIdx.y * per, j1 = j0 + per < cnt + 1 ? j0 + per : cnt + 1;
+    for (int c0 = 0; c0 < a.d; c0 += 32) {
+        const int c = c0 + threadIdx.x;
+        float s = 0.f;
+        if (c < a.d) {
+            if (threadIdx.y == 0) s = a.partial[(w * 2 + 1) * a.d + c];
+#pragma unroll 8
+            for (long long j = j0; j < j1; ++j) s += a.partial[(w + j) * 2 * a.d + c];
+        }
+        part[threadIdx.y][threadIdx.x] = s;
+        __syncthreads();
+        if (threadIdx.y == 0 && c < a.d) {
+            s = part[0][threadIdx.x];
+#pragma unroll
+            for (int q = 1; q < 8; ++q) s += part[q][threadIdx.x];
+            static_cast<TO*>(a.dT)[(long long)key * a.d + c] = Cvt<TO>::from_f(s * a.scale);
+        }
+        __syncthreads();
+    }
+}
+
+// Pairs per window: short windows while long ones would leave SMs without work.
+int window_len(long long n, int d) { return n * (long long)d >= (1ll << 24) ? 64 : 16; }
+
+template <typename TI, typename TO, int VEC>
+dlrm_status sum_vec(SumArgs a, cudaStream_t st) {
+    const int runs = a.d / VEC;
+    const int tx = pow2_at_least(runs, 128);
+    const dim3 block(tx, 128 / tx);
+    a.slices = (runs + tx - 1) / tx;
+    const long long wblocks = (a.windows + block.y - 1) / block.y * a.slices;
+    // zero rows: a warp per 32 rows, up to eight blocks per SM
+    const long long zblocks = std::min<long long>((a.m + 127) / 128, 8ll * device_sms());
+    if (wblocks + zblocks > (1ll << 31) - 1) return DLRM_ERR_UNSUPPORTED;
+    a.wblocks = (int)wblocks;
+    DLRM_PDL_CHECK(launch_pdl(run_sum_kernel<TI, TO, VEC>, dim3((unsigned)(wblocks + zblocks)), block, 0, st, a));
+    if (a.windows > 1)
+        DLRM_PDL_CHECK(launch_pdl(run_join_kernel<TO>, dim3((unsigned)(a.windows - 1)), dim3(32, 8), 0, st, a));
+    return DLRM_OK;
+}
+
+template <typename TI, typename TO>
+dlrm_status sum_to(const SumArgs& a, cudaStream_t st) {
+    constexpr int W = 16 / (int)(sizeof(TI) < sizeof(TO) ? sizeof(TI) : sizeof(TO));
+    auto fits = [&](int vec) {
+        const int bi = std::min(16, vec * (int)sizeof(TI)), bo = std::min(16, vec * (int)sizeof(TO));
+        return a.d % vec == 0 && rows_on(a.dout, a.ldd * (long long)sizeof(TI), bi) &&
+               rows_on(a.dT, (long long)a.d * sizeof(TO), bo);
+    };
+    if (fits(W)) return sum_vec<TI, TO, W>(a, st);
+    if (fits(2)) return sum_vec<TI, TO, 2>(a, st);
+    return sum_vec<TI, TO, 1>(a, st);
+}
+
+template <typename TI>
+dlrm_status sum_ti(const SumArgs& a, dlrm_dtype dt, cudaStream_t st) {
+    if (dt == DLRM_F32) return sum_to<TI, float>(a, st);
+    if (dt == DLRM_F16) return sum_to<TI, __half>(a, st);
+    return sum_to<TI, __nv_bfloat16>(a, st);
+}
+
+struct GradLayout {
+    int nblocks, passes, bits;
+    long long chunk;
+    size_t keys[2], vals[2], hist, partial, total;
+};
+
+GradLayout grad_layout(long long m, int d, long long n) {
+    GradLayout L;
+    int kb = 1;
+    while ((1ll << kb) <= m) ++kb;             // ids 0 .. m
+    L.passes = n <= SORT1_MAX ? 0 : (kb + DIG_BITS_MAX - 1) / DIG_BITS_MAX;
+    L.bits = L.passes ? (kb + L.passes - 1) / L.passes : 0;
+    const long long tiles = (n + RS_TILE - 1) / RS_TILE;
+    const long long per = (tiles + RS_BLOCKS_MAX - 1) / RS_BLOCKS_MAX;
+    L.chunk = std::max(1ll, per) * RS_TILE;
+    L.nblocks = (int)std::max(1ll, (n + L.chunk - 1) / L.chunk);
+    size_t off = align_up(DLRM_ERR_RECORD_BYTES, 256);
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = align_up(off + bytes, 256);
+        return o;
+    };
+    const int pairs = L.passes ? 2 : 1;
+    for (int i = 0; i < 2; ++i) L.keys[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
+    for (int i = 0; i < 2; ++i) L.vals[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
+    L.hist = take(L.passes ? sizeof(int) * ((size_t)L.nblocks << L.bits) : 0);
+    const long long windows = (n + window_len(n, d) - 1) / window_len(n, d);
+    L.partial = take(sizeof(float) * 2 * (size_t)windows * d);
+    L.total = off;
+    return L;
+}
+
+}  // namespace
+
+dlrm_status launch_lookup(const void* table, dlrm_dtype dt, long long rows, int d, long long n, const int32_t* idx,
+                          float scale, void* out, long long ldo, dlrm_dtype out_dt, ErrRecord* err, cudaStream_t st) {
+    const LookupArgs a{n, d, rows, table, idx, scale, out, ldo, err};
+    if (dt == DLRM_F32) return lookup_ti<float>(a, out_dt, st);
+    if (dt == DLRM_F16) return lookup_ti<__half>(a, out_dt, st);
+    return lookup_ti<__nv_bfloat16>(a, out_dt, st);
+}
+
+size_t lookup_grad_workspace(long long m, int d, long long n) { return grad_layout(m, d, n).total; }
+
+dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* idx, float scale, const void* dout,
+                               long long ldd, dlrm_dtype dt, void* dT, dlrm_dtype dT_dt, char* ws, cudaStream_t st) {
+    const GradLayout L = grad_layout(m, d, n);
+    ErrRecord* err = reinterpret_cast<ErrRecord*>(ws);
+    uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + L.keys[0]), reinterpret_cast<uint32_t*>(ws + L.keys[1])};
+    uint32_t* vals[2] = {reinterpret_cast<uint32_t*>(ws + L.vals[0]), reinterpret_cast<uint32_t*>(ws + L.vals[1])};
+    int* hist = reinterpret_cast<int*>(ws + L.hist);
+    int cur = 0;
+    if (L.passes == 0) {
+        if (n > 0) {
+            int padded = 2;
+            while (padded < n) padded <<= 1;
+            const int threads = std::max(32, std::min(1024, padded / 2));
+            DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1), dim3(threads), sizeof(unsigned long long) * padded,
+                                      st, (int)n, padded, m, idx, keys[0], vals[0], err));
+        }
+    } else {
+        const dim3 grid(L.nblocks), block(RS_THREADS);
+        for (int p = 0; p < L.passes; ++p) {
+            const int shift = p * L.bits;
+            if (p == 0) {
+                DLRM_PDL_CHECK(launch_pdl(rs_hist_kernel<true>, grid, block, 0, st, n, m, (const void*)idx, shift,
+                                          L.bits, L.chunk, hist, err));
+                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<true>, grid, block, 0, st, n, m, (const void*)idx,
+                                          (const uint32_t*)nullptr, shift, L.bits, L.chunk, (const int*)hist, keys[0],
+                                          vals[0]));
+            } else {
+                DLRM_PDL_CHECK(launch_pdl(rs_hist_kernel<false>, grid, block, 0, st, n, m, (const void*)keys[cur], shift,
+                                          L.bits, L.chunk, hist, err));
+                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<false>, grid, block, 0, st, n, m, (const void*)keys[cur],
+                                          (const uint32_t*)vals[cur], shift, L.bits, L.chunk, (const int*)hist,
+                                          keys[cur ^ 1], vals[cur ^ 1]));
+                cur ^= 1;
+            }
+        }
+    }
+    SumArgs a;
+    a.n = n;
+    a.m = m;
+    a.d = d;
+    a.P = window_len(n, d);
+    a.windows = (n + a.P - 1) / a.P;
+    a.wblocks = a.slices = 0;
+    a.keys = keys[cur];
+    a.vals = vals[cur];
+    a.dout = dout;
+    a.ldd = ldd;
+    a.scale = scale;
+    a.partial = reinterpret_cast<float*>(ws + L.partial);
+    a.dT = dT;
+    if (dt == DLRM_F32) return sum_ti<float>(a, dT_dt, st);
+    if (dt == DLRM_F16) return sum_ti<__half>(a, dT_dt, st);
+    return sum_ti<__nv_bfloat16>(a, dT_dt, st);
+}
+
+}  // namespace dlrm

@@ -55,6 +55,7 @@ extern "C" {
 #define DLRM_MAX_TABLES 256
 #define DLRM_MAX_LAYERS 16
 #define DLRM_ERR_RECORD_BYTES 256
+#define DLRM_MAX_EXPERTS 256
 
 typedef struct CUstream_st* dlrm_stream; /* a cudaStream_t */
 
@@ -77,8 +78,13 @@ typedef enum {
  * of the parameters ([N] Key Method Details); storing rows at ~1.1 bytes per
  * value instead of 2 cuts the gathered bytes. Supported by the fused gather +
  * interaction path (dlrm_embbag_interact_fwd, dlrm_forward) for d = 64 or 128;
- * other entry points return DLRM_ERR_UNSUPPORTED for it. */
-typedef enum { DLRM_F32 = 0, DLRM_F16 = 1, DLRM_BF16 = 2, DLRM_U8ROW = 3 } dlrm_dtype;
+ * other entry points return DLRM_ERR_UNSUPPORTED for it.
+ *
+ * DLRM_E4M3 (dlrm_rmsnorm_fwd's output and dlrm_experts_fwd's operands only;
+ * other entry points refuse it): 8-bit floating point, 4 exponent and 3
+ * mantissa bits, no infinity, largest value 448. Rows of codes come with one
+ * fp32 scale per row; the value of a code q is scale * q. */
+typedef enum { DLRM_F32 = 0, DLRM_F16 = 1, DLRM_BF16 = 2, DLRM_U8ROW = 3, DLRM_E4M3 = 4 } dlrm_dtype;
 
 typedef enum { DLRM_ACT_NONE = 0, DLRM_ACT_RELU = 1, DLRM_ACT_SIGMOID = 2 } dlrm_act;
 
@@ -404,6 +410,118 @@ size_t dlrm_embbag_sgd_scratch_size(const dlrm_tables* T, int B, int64_t nnz);
 dlrm_status dlrm_embbag_sgd(const dlrm_tables* T, int B, const int32_t* offsets, const int32_t* indices, int64_t nnz,
                             const float* dE, float lr, void* scratch, size_t scratch_bytes, int32_t* n_touched,
                             dlrm_stream stream);
+
+/* ------------------------------------------------------------ token blocks
+ * What a ranking model over sequences of ids, or one whose towers are routed
+ * experts, runs next to the pooled path: unpooled lookups with their
+ * gradient, dropout, a root-mean-square norm with the residual's addition, and
+ * fully connected layers grouped by expert. The pages describe no counterpart.
+ * Shared by these calls:
+ *  - A matrix comes as a pointer, its row pitch `ld` in elements and its
+ *    logical width; elements from the width to ld are neither read nor
+ *    written. Matrices of dlrm_experts_* follow the 16-byte rules above; those
+ *    of the other calls may have any pitch >= the width and any address that is
+ *    a multiple of the element size (rows on 16-byte boundaries are fastest).
+ *  - Sums and statistics are fp32; each output is rounded to its type once.
+ *    Results do not depend on timing: the same call gives the same bits.
+ *  - Sizes of zero (n, rows, M) are valid and launch what the outputs still
+ *    need (zero gradients), or nothing.
+ *  - Calls that share a workspace, or that write the same outputs, must follow
+ *    one another on one stream; this includes replays of captured graphs. */
+
+/* Lookup with scaling: out[i] = scale * T_k[indices[i]], i < n, for table k of
+ * T (any d >= 1 up to 65,536 here; T->rows[k] < 2^31; DLRM_U8ROW:
+ * DLRM_ERR_UNSUPPORTED). An index outside [0, T->rows[k]) gives a row of zeros
+ * and is counted in the error record.
+ *   indices  int32 [n], n < 2^31
+ *   out      [n][ld_out] of out_dt (fp32, fp16 or bf16, whatever the table's)
+ *   ws       ws_bytes >= DLRM_ERR_RECORD_BYTES */
+dlrm_status dlrm_embed_fwd(const dlrm_tables* T, int k, int64_t n, const int32_t* indices, float scale, void* out,
+                           int64_t ld_out, dlrm_dtype out_dt, void* ws, size_t ws_bytes, dlrm_stream stream);
+
+/* Its gradient with respect to the table, by sorted ids: every row r < rows of
+ *   dtable[r] = scale * sum of dout[i] over the i with indices[i] = r
+ * is written (zeros where there is none), the sum in fp32 over increasing i
+ * (in fixed pieces whose sums are added in order). Indices outside [0, rows)
+ * contribute nothing and are counted.
+ *   dout    [n][ld_dout] of dout_dt;  dtable [rows][d] of dtable_dt, dense
+ *   ws      16-byte aligned, dlrm_embed_bwd_workspace_size(rows, d, n) bytes */
+size_t dlrm_embed_bwd_workspace_size(int64_t rows, int d, int64_t n);
+dlrm_status dlrm_embed_bwd(int64_t rows, int d, int64_t n, const int32_t* indices, float scale, const void* dout,
+                           int64_t ld_dout, dlrm_dtype dout_dt, void* dtable, dlrm_dtype dtable_dt, void* ws,
+                           size_t ws_bytes, dlrm_stream stream);
+
+/* Dropout with a counter-based generator, over n dense elements of dt:
+ *   y[i] = [residual[i] +] (word_i >= p 2^32 ? x[i] / (1 - p) : 0)
+ * word_i is 32-bit word i mod 4 of Philox4x32-10 (Salmon et al., "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011) for the counter with low half i / 4
+ * and high half offset, and the key seed. No mask is stored: the gradient of x
+ * is the same call on dy with the same rng and no residual.
+ *   rng  device, int64 {seed, offset}: read when the kernel runs, so a captured
+ *        graph draws anew when they change between replays
+ *   0 <= p <= 1 (1 drops everything); a dropped element is 0 whatever x holds;
+ *   residual optional; y may be x or residual. */
+dlrm_status dlrm_dropout(int64_t n, const void* x, const void* residual, dlrm_dtype dt, double p, const int64_t* rng,
+                         void* y, dlrm_stream stream);
+
+/* Root-mean-square norm with the residual's addition, per row of d <= 32,768:
+ *   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * w
+ * in fp32 from the unrounded h.
+ *   x, residual (optional), h (optional): [rows][ld] of dt (fp32, fp16, bf16);
+ *     h may be x's or residual's own buffer
+ *   w        fp32 [d], or NULL for ones;  eps >= 0
+ *   y        [rows][ld_y] of y_dt: dt, or DLRM_E4M3 with
+ *   y_scale  fp32 [rows] (DLRM_E4M3 only): max|y| / 448; the codes are y / y_scale
+ *            rounded to nearest. A row of zeros has scale 0 and codes 0; an
+ *            infinity or NaN in a row makes its scale one, and with it all of it.
+ *   rstd     fp32 [rows], optional (the backward pass takes it) */
+dlrm_status dlrm_rmsnorm_fwd(int rows, int d, const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                             dlrm_dtype dt, const float* w, float eps, void* h, int64_t ld_h, void* y, int64_t ld_y,
+                             dlrm_dtype y_dt, float* y_scale, float* rstd, dlrm_stream stream);
+
+/* Gradient of the above from what the forward stored (h as rounded, rstd):
+ *   xh = h * rstd;  dx = rstd * (dy w - xh mean(dy w xh)) + dh;  dw = sum over rows of dy xh
+ * dx is the gradient of x and of residual alike. dh (optional): the gradient
+ * that reaches h by other ways (the residual stream). dw (optional): fp32 [d].
+ * dx may be dy's or dh's own buffer.
+ *   ws  16-byte aligned, dlrm_rmsnorm_bwd_workspace_size(rows, d) bytes */
+size_t dlrm_rmsnorm_bwd_workspace_size(int rows, int d);
+dlrm_status dlrm_rmsnorm_bwd(int rows, int d, const void* dy, int64_t ld_dy, const void* h, int64_t ld_h,
+                             const float* rstd, const float* w, const void* dh, int64_t ld_dh, dlrm_dtype dt, void* dx,
+                             int64_t ld_dx, float* dw, void* ws, size_t ws_bytes, dlrm_stream stream);
+
+/* Fully connected layers grouped by expert, ragged: expert e has weights
+ * W_e = W + e * N * ldw ([N][ldw], as a layer of dlrm_mlp) and rows
+ * [offsets[e], offsets[e + 1]) of X and Y:
+ *   Y_r = act(X_r W_e^T + bias_e),  fp32 accumulation.
+ * Rows outside every expert's range are not written.
+ *   offsets  device int32 [E + 1], E <= DLRM_MAX_EXPERTS. A range that decreases,
+ *            leaves [0, M] or starts below an earlier offset counts as empty, and
+ *            as a bad bag in the error record.
+ *   X        [M][ldx] of dt: fp16, bf16, or DLRM_E4M3 with x_scale fp32 [M]
+ *   W        of dt;  DLRM_E4M3: w_scale fp32 [E][N], one per weight row
+ *   bias     fp32 [E][N], optional;  act DLRM_ACT_NONE or DLRM_ACT_RELU
+ *   Y        [M][ldy] of y_dt: dt or fp32 (DLRM_E4M3 operands: fp32, fp16 or bf16)
+ *   ws       ws_bytes >= DLRM_ERR_RECORD_BYTES
+ * fp32 operands: DLRM_ERR_UNSUPPORTED (dlrm_gemm_f32 is the fp32 product). */
+dlrm_status dlrm_experts_fwd(int E, int M, int N, int K, const int32_t* offsets, const void* X, int64_t ldx,
+                             const float* x_scale, dlrm_dtype dt, const void* W, int64_t ldw, const float* w_scale,
+                             const float* bias, int act, void* Y, int64_t ldy, dlrm_dtype y_dt, void* ws,
+                             size_t ws_bytes, dlrm_stream stream);
+
+/* Its gradients (fp16 and bf16). With dP = dY, or dY where Y > 0 for
+ * DLRM_ACT_RELU (Y: the forward's output in dt):
+ *   dX_r = dP_r W_e (rows outside every range are not written);
+ *   dW_e = sum over e's rows of dP_r^T X_r;  db_e = sum of dP_r
+ * (zeros for an expert without rows). dX, dW and db are each optional.
+ *   dX  [M][lddx] of dx_dt: dt or fp32;  dW [E][N][lddw] of dw_dt: dt or fp32
+ *   db  fp32 [E][N];  X is needed for dW only, W for dX only
+ *   ws  16-byte aligned, dlrm_experts_bwd_workspace_size(E, M, N, K, act) bytes */
+size_t dlrm_experts_bwd_workspace_size(int E, int M, int N, int K, int act);
+dlrm_status dlrm_experts_bwd(int E, int M, int N, int K, const int32_t* offsets, const void* dY, int64_t lddy,
+                             const void* Y, int64_t ldy, int act, const void* X, int64_t ldx, const void* W,
+                             int64_t ldw, dlrm_dtype dt, void* dX, int64_t lddx, dlrm_dtype dx_dt, void* dW,
+                             int64_t lddw, dlrm_dtype dw_dt, float* db, void* ws, size_t ws_bytes, dlrm_stream stream);
 
 /* Size of the device scratch array that dlrm_forward_noalloc uses (32 MiB). */
 #define DLRM_NOALLOC_SCRATCH_BYTES (32u << 20)
