@@ -522,10 +522,13 @@ def _matrix(t, where: str, rows: int, cols: int):
     """(pointer, row pitch) of a [rows][cols] tensor whose rows are contiguous."""
     if t is None:
         return None, cols
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+    if t.shape != (rows, cols):
+        _refuse(where)
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         _refuse(where)
     # the pitch of a single row says nothing: any pitch that keeps the alignment rules will do
-    return _ptr(t), (t.stride(0) if rows > 1 else (cols + 15) // 16 * 16)
+    return (t.data_ptr() if rows else None), (ld if rows > 1 else (cols + 15) // 16 * 16)
 
 
 def _stacked(t, where: str, n: int, rows: int, cols: int):
@@ -561,30 +564,34 @@ def _float_code(t, where: str) -> int:
     return code
 
 
-def _same_device(where: str, *tensors):
-    """The one CUDA device every given tensor is on."""
-    dev = None
+def _same_device(where: str, *tensors) -> int:
+    """The number of the one CUDA device every given tensor is on."""
+    dev = -1
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or (dev is not None and t.device != dev):
-            _refuse(where)
-        dev = t.device
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or (dev >= 0 and d != dev):
+                _refuse(where)
+            dev = d
     return dev
 
 
-def _call(where: str, dev, stream, fn, *args):
+def _call(where: str, dev: int, stream, fn, *args):
     """Runs a C entry point on the tensors' device, which need not be the current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device != dev:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
             _refuse(where)
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        return _check(fn(*args, C.c_void_p(int(stream))), where)
-    with torch.cuda.device(dev):
-        return _check(fn(*args, C.c_void_p(int(stream))), where)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != OK:
+        raise DlrmError(status, where)
+    return status
 
 
 def dlrm_embed_fwd(T: Tables, k: int, indices, out, ws, scale: float = 1.0, stream=None):

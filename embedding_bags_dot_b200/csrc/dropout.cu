@@ -20,19 +20,28 @@
 namespace dlrm {
 namespace {
 
-__device__ __forceinline__ uint4 philox4x32_10(unsigned long long group, uint32_t c2, uint32_t c3, uint32_t k0,
-                                               uint32_t k1) {
+// The ten rounds' keys, the same for every element.
+struct RoundKeys {
+    uint32_t a[10], b[10];
+    __device__ __forceinline__ RoundKeys(unsigned long long seed) {
+#pragma unroll
+        for (int r = 0; r < 10; ++r) {
+            a[r] = (uint32_t)seed + 0x9E3779B9u * r;
+            b[r] = (uint32_t)(seed >> 32) + 0xBB67AE85u * r;
+        }
+    }
+};
+
+__device__ __forceinline__ uint4 philox4x32_10(unsigned long long group, uint32_t c2, uint32_t c3, const RoundKeys& k) {
     uint32_t c0 = (uint32_t)group, c1 = (uint32_t)(group >> 32);
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const unsigned long long a = (unsigned long long)0xD2511F53u * c0;
         const unsigned long long b = (unsigned long long)0xCD9E8D57u * c2;
-        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k.a[r];
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k.b[r];
         c1 = (uint32_t)b;
         c3 = (uint32_t)a;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     return make_uint4(c0, c1, c2, c3);
 }
@@ -57,43 +66,52 @@ __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ Dr
     const T* res = static_cast<const T*>(a.residual);
     T* y = static_cast<T*>(a.y);
     const unsigned long long seed = a.rng[0], off = a.rng[1];
-    const uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32), c2 = (uint32_t)off, c3 = (uint32_t)(off >> 32);
-    const long long stride = (long long)gridDim.x * blockDim.x * VEC;
-    for (long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * VEC; i < a.n; i += stride) {
-        const bool whole = ALIGNED && i + VEC <= a.n;
-        RowRaw<T, VEC> rx, rr;
-        if (whole) {
-            rx.load(x + i);
-            if constexpr (RES) rr.load(res + i);
-        } else {
+    const RoundKeys keys(seed);
+    const uint32_t c2 = (uint32_t)off, c3 = (uint32_t)(off >> 32);
+    // a block's turn: two runs per thread, loaded together
+    for (long long turn = blockIdx.x; turn * (2 * VEC * 256) < a.n; turn += gridDim.x) {
+        RowRaw<T, VEC> rx[2], rr[2];
+        const long long i0 = (turn * 512 + threadIdx.x) * VEC;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (i + e < a.n) {
-                    rx.e[e] = x[i + e];
-                    if constexpr (RES) rr.e[e] = res[i + e];
-                }
-        }
-        float v[VEC];
+        for (int u = 0; u < 2; ++u) {
+            const long long i = i0 + u * (256 * VEC);
+            if (ALIGNED && i + VEC <= a.n) {
+                rx[u].load(x + i);
+                if constexpr (RES) rr[u].load(res + i);
+            } else {
 #pragma unroll
-        for (int g = 0; g < VEC / 4; ++g) {
-            const uint4 w = philox4x32_10((unsigned long long)(i / 4 + g), c2, c3, k0, k1);
-            const uint32_t word[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // a dropped element gives zero whatever x holds there (infinity and NaN too)
-                const int q = 4 * g + e;
-                v[q] = word[e] >= a.threshold && a.any ? Cvt<T>::to_f(rx.e[q]) * a.scale : 0.f;
-                if constexpr (RES) v[q] += Cvt<T>::to_f(rr.e[q]);
+                for (int e = 0; e < VEC; ++e)
+                    if (i + e < a.n) {
+                        rx[u].e[e] = x[i + e];
+                        if constexpr (RES) rr[u].e[e] = res[i + e];
+                    }
             }
         }
-        RowRaw<T, VEC> out;
-        out.set(v);
-        if (whole) {
-            out.store(y + i);
-        } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (i + e < a.n) y[i + e] = out.e[e];
+        for (int u = 0; u < 2; ++u) {
+            const long long i = i0 + u * (256 * VEC);
+            float v[VEC];
+#pragma unroll
+            for (int g = 0; g < VEC / 4; ++g) {
+                const uint4 w = philox4x32_10((unsigned long long)(i / 4 + g), c2, c3, keys);
+                const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // a dropped element gives zero whatever x holds there (infinity and NaN too)
+                    const int q = 4 * g + e;
+                    v[q] = word[e] >= a.threshold && a.any ? Cvt<T>::to_f(rx[u].e[q]) * a.scale : 0.f;
+                    if constexpr (RES) v[q] += Cvt<T>::to_f(rr[u].e[q]);
+                }
+            }
+            RowRaw<T, VEC> out;
+            out.set(v);
+            if (ALIGNED && i + VEC <= a.n) {
+                out.store(y + i);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (i + e < a.n) y[i + e] = out.e[e];
+            }
         }
     }
 }
@@ -102,8 +120,8 @@ template <typename T>
 dlrm_status launch_t(const DropArgs& a, cudaStream_t st) {
     const bool al = rows_on(a.x, 0, 16) && rows_on(a.y, 0, 16) && rows_on(a.residual, 0, 16);
     const int vec = al ? 16 / (int)sizeof(T) : 4;
-    const long long want = (a.n + 256ll * vec - 1) / (256ll * vec);
-    const long long most = 16ll * device_sms();
+    const long long want = (a.n + 512ll * vec - 1) / (512ll * vec);
+    const long long most = 8ll * device_sms();
     const dim3 grid((unsigned)(want < most ? want : most));
 #define DLRM_DROP(RES, AL) DLRM_PDL_CHECK(launch_pdl(dropout_kernel<T, RES, AL>, grid, dim3(256), 0, st, a))
     if (a.residual) {

@@ -20,10 +20,11 @@
 // Two kernels on tcgen05 with TMA-fed 128-byte-swizzled shared memory:
 //  - expert_pair_kernel: 256 x 256 tiles on SM pairs (cta_group::2), all three
 //    products. Bound by the tensor pipe at large sizes.
-//  - expert_tile_kernel: 128 x 64 or 128 x 128 tiles on one SM, forward only, for
-//    calls too small to fill the pairs; with few rows the weights are all the
-//    traffic and narrow tiles put more SMs to reading them. A row block of at
-//    most 32 rows loads 32 rows instead of 128.
+//  - expert_tile_kernel: tiles of 128 rows and 64 or 128 columns on one SM,
+//    forward only, for calls too small to fill the pairs, where reading the
+//    weights bounds the time. A row block of at most 32 rows loads 32 rows
+//    instead of 128. Calls of at most 32 rows (single tokens) take 32-column
+//    tiles with three quarters of the shared memory filled by weights on their way.
 // The tensor core truncates as it accumulates, so no accumulator runs longer
 // than 8 k-blocks (512 16-bit or 1,024 8-bit terms): the epilogue warps add each
 // finished part to fp32 registers, rounding to nearest, while the next part
@@ -43,11 +44,22 @@ namespace tc {
 
 constexpr int EX_MAX = DLRM_MAX_EXPERTS;
 constexpr int PART = 8;                             // k-blocks per accumulator
+#ifndef EX_FEWW
+#define EX_FEWW 32
+#endif
 constexpr int EX_THREADS2 = 384;                    // pair kernel: warps 0..3 TMA, MMA, idle; 4..11 epilogue
 constexpr int EX_REGS_LOW = 40, EX_REGS_HIGH = 232;
 static_assert(128 * EX_REGS_LOW + 256 * EX_REGS_HIGH <= 168 * EX_THREADS2, "register split exceeds the launch allocation");
-constexpr int EX_STAGES2 = 6;
 constexpr int EX_STAGE2_BYTES = 32768;              // 128 rows x 128 bytes of A, as much of B
+// Shared memory of the pair kernel: 16-bit operands take five stages and two output buffers per epilogue warp, so
+// that a warp's next 128 bytes of columns need not wait for the last store to be read; 8-bit stages are used up
+// twice as fast and get six, with one output buffer.
+template <int KIND>
+struct ExPair {
+    static constexpr int NS = KIND == 0 ? 5 : 6;
+    static constexpr int NOUT = KIND == 0 ? 2 : 1;
+    static constexpr int OUT = EPI_WARPS * NOUT * STAGE_OUT_BYTES;
+};
 
 enum ExpertOp { EX_FWD = 0, EX_DGRAD = 1, EX_WGRAD = 2 };
 enum ExpertKind { EX_F16 = 0, EX_F8 = 1 };
@@ -165,6 +177,18 @@ __host__ __device__ constexpr uint32_t ex_idesc(int fmt, bool a_mn, bool b_mn, i
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// The TMA and MMA warps run their loops with all lanes and issue from one elected lane: what the instructions
+// take (descriptors, coordinates, addresses) is then the same for the warp and stays in uniform registers.
+// Issued from a one-lane branch instead, a k-block of four MMAs took 640 cycles whatever its width (measured with
+// the clock at 32, 64 and 128 columns), most of it moving operands into uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint64_t desc64(uint32_t hi, uint32_t lo) { return ((uint64_t)hi << 32) | lo; }
+
 template <int KIND, int CG>
 __device__ __forceinline__ void ex_umma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
     if constexpr (KIND == EX_F16 && CG == 2) {
@@ -206,53 +230,100 @@ __device__ __forceinline__ void ex_store_3d(const CUtensorMap* map, uint32_t src
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// acc[c] += the 32 TMEM columns at taddr + 32 c
+// 32 TMEM columns straight into fp32 registers (valid after tmem_ld_wait)
+__device__ __forceinline__ void tmem_ld32_f(uint32_t taddr, float (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%"
+        "19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr));
+}
+
+// acc[c] += the 32 TMEM columns at taddr + 32 c, two loads in flight
 template <int NC>
 __device__ __forceinline__ void ex_promote(float (&acc)[NC][32], uint32_t taddr) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        uint32_t r[32];
-        tmem_ld32_issue(taddr + 32 * c, r);
+    for (int c = 0; c < NC; c += 2) {
+        constexpr int W = NC < 2 ? NC : 2;
+        float r[W][32];
+#pragma unroll
+        for (int i = 0; i < W; ++i) tmem_ld32_f(taddr + 32 * (c + i), r[i]);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) acc[c][e] += __uint_as_float(r[e]);
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[c + i][e] += r[i][e];
+    }
+}
+
+// What the forward's epilogue needs besides the sums, fetched while the tile is still being multiplied: lane l
+// holds the bias and weight scale of column 32 c + l of each 32-column group c, and the scale of its row.
+template <int NC>
+struct EpiRow {
+    float bias[NC], wsc[NC], xs;
+};
+template <int NC, int OP, int KIND>
+__device__ __forceinline__ void ex_fetch(EpiRow<NC>& er, int row0, int nvalid, int j0, int e, const ExpertArgs& a) {
+    if constexpr (OP == EX_FWD) {
+        const int lane = threadIdx.x & 31;
+        er.xs = KIND == EX_F8 && lane < nvalid ? __ldg(a.x_scale + row0 + lane) : 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int col = j0 + 32 * c + lane;
+            const bool in = col < a.J;
+            er.bias[c] = a.bias && in ? __ldg(a.bias + (long long)e * a.J + col) : 0.f;
+            er.wsc[c] = KIND == EX_F8 && in ? __ldg(a.w_scale + (long long)e * a.J + col) : 0.f;
+        }
+    }
+}
+
+// Scales, bias and ReLU of 32 columns (group g of the warp's).
+template <int NC, int KIND>
+__device__ __forceinline__ void ex_affine(float (&v)[32], const EpiRow<NC>& er, int g, const ExpertArgs& a) {
+    if constexpr (KIND == EX_F8) {
+#pragma unroll
+        for (int q = 0; q < 32; ++q) v[q] *= er.xs * __shfl_sync(0xffffffffu, er.wsc[g], q);
+    }
+    if (a.bias) {
+#pragma unroll
+        for (int q = 0; q < 32; ++q) v[q] += __shfl_sync(0xffffffffu, er.bias[g], q);
+    }
+    if (a.relu) {
+        // not fmaxf: a NaN stays one
+#pragma unroll
+        for (int q = 0; q < 32; ++q) v[q] = v[q] < 0.f ? 0.f : v[q];
     }
 }
 
 // One warp's share of a finished tile: 32 rows (one per lane) x 32 NC columns from column j0. Rows go out
 // through the warp's 4 KB stage, 128 bytes of columns at a time: whole 32-row groups by TMA (columns
 // past J are clipped), a group that holds the expert's last row by 16-byte stores of its valid rows only.
-//   row0: first output row of the warp; nvalid: its rows that exist (<= 0: none); z: expert (wgrad)
-template <typename TC, int NC, int OP, int KIND>
-__device__ __forceinline__ void ex_store(float (&acc)[NC][32], int row0, int nvalid, int j0, int e, const ExpertArgs& a,
-                                         const CUtensorMap* mapC, unsigned char* stage, uint32_t stage_s) {
+//   row0: first output row of the warp; nvalid: its rows that exist (<= 0: none); e: expert
+//   buf: which of the warp's NOUT output buffers comes next
+template <typename TC, int NC, int OP, int KIND, int NOUT>
+__device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>& er, int row0, int nvalid, int j0, int e,
+                                         const ExpertArgs& a, const CUtensorMap* mapC, unsigned char* stage0,
+                                         uint32_t stage_s0, int& buf) {
     constexpr int CW = 128 / (int)sizeof(TC);   // columns per 128 bytes: 32 (fp32) or 64
     constexpr int PER = CW / 32;                // 32-column groups per 128 bytes
     const int lane = threadIdx.x & 31;
     if (nvalid <= 0) return;                    // uniform across the warp
-    float xs = 1.f;
-    if constexpr (KIND == EX_F8) xs = lane < nvalid ? a.x_scale[row0 + lane] : 0.f;
 #pragma unroll
     for (int c = 0; c < NC / PER; ++c) {
         const int n0 = j0 + c * CW;
         if (n0 >= a.J) break;                   // uniform across the warp
         if constexpr (OP == EX_FWD) {
-            const float* bias = a.bias ? a.bias + (long long)e * a.J : nullptr;
-            const float* wsc = KIND == EX_F8 ? a.w_scale + (long long)e * a.J : nullptr;
 #pragma unroll
-            for (int p = 0; p < PER; ++p)
-#pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                    const int col = n0 + 32 * p + q;
-                    const bool in = col < a.J;
-                    float& v = acc[c * PER + p][q];
-                    if constexpr (KIND == EX_F8) v *= xs * (in ? __ldg(wsc + col) : 0.f);
-                    if (bias) v += in ? __ldg(bias + col) : 0.f;
-                    // not fmaxf: a NaN stays one
-                    if (a.relu) v = v < 0.f ? 0.f : v;
-                }
+            for (int p = 0; p < PER; ++p) ex_affine<NC, KIND>(acc[c * PER + p], er, c * PER + p, a);
         }
-        if (lane == 0) bulk_wait_read0();       // the previous chunk's store has read the stage
+        unsigned char* stage = stage0 + buf * STAGE_OUT_BYTES;
+        const uint32_t stage_s = stage_s0 + buf * STAGE_OUT_BYTES;
+        buf = buf + 1 == NOUT ? 0 : buf + 1;
+        // the store that last used this buffer has read it: at most NOUT - 1 are still to be read
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(NOUT - 1) : "memory");
         __syncwarp();
         unsigned char* row = stage + lane * 128;
 #pragma unroll
@@ -260,11 +331,12 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], int row0, int nva
             uint4 w;
             if constexpr (sizeof(TC) == 2) {
                 union {
-                    TC t[8];
+                    uint32_t t[4];
                     uint4 w;
                 } u;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) u.t[k] = Cvt<TC>::from_f(acc[c * PER + q / 4][(q % 4) * 8 + k]);
+                for (int k = 0; k < 8; k += 2)
+                    u.t[k / 2] = Pair<TC>::from_f(acc[c * PER + q / 4][(q % 4) * 8 + k], acc[c * PER + q / 4][(q % 4) * 8 + k + 1]);
                 w = u.w;
             } else {
                 w = make_uint4(__float_as_uint(acc[c][4 * q]), __float_as_uint(acc[c][4 * q + 1]),
@@ -304,6 +376,33 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], int row0, int nva
     }
 }
 
+// At most 32 rows x 32 columns, straight from registers: each lane writes its row's 64 or 128 bytes.
+template <typename TC, int KIND>
+__device__ __forceinline__ void ex_store_few(float (&v)[32], const EpiRow<1>& er, int row0, int nvalid, int j0,
+                                             const ExpertArgs& a) {
+    const int lane = threadIdx.x & 31;
+    ex_affine<1, KIND>(v, er, 0, a);
+    if (lane >= nvalid) return;
+    TC* dst = static_cast<TC*>(a.C) + (long long)(row0 + lane) * a.ldc + j0;
+    constexpr int E16 = 16 / (int)sizeof(TC);
+#pragma unroll
+    for (int q = 0; q < 32 / E16; ++q) {
+        union {
+            TC t[E16];
+            uint4 w;
+        } u;
+#pragma unroll
+        for (int k = 0; k < E16; ++k) u.t[k] = Cvt<TC>::from_f(v[q * E16 + k]);
+        if (j0 + (q + 1) * E16 <= a.J) {
+            *reinterpret_cast<uint4*>(dst + q * E16) = u.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < E16; ++k)
+                if (j0 + q * E16 + k < a.J) dst[q * E16 + k] = u.t[k];
+        }
+    }
+}
+
 // k-blocks of a tile: the reduction length of fwd and dgrad, the expert's rows in wgrad.
 template <int OP, int KIND>
 __device__ __forceinline__ int ex_kblocks(const ExpertArgs& a, int rows) {
@@ -320,14 +419,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
     const uint32_t raw = su32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* gbase = smem_raw + (base - raw);
-    Ranges* rg = reinterpret_cast<Ranges*>(gbase + EX_STAGES2 * EX_STAGE2_BYTES + OUT_BYTES);
-    ExBars<EX_STAGES2>* bars = reinterpret_cast<ExBars<EX_STAGES2>*>(rg + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    using P = ExPair<KIND>;
+    constexpr int NS = P::NS;
+    Ranges* rg = reinterpret_cast<Ranges*>(gbase + NS * EX_STAGE2_BYTES + P::OUT);
+    ExBars<NS>* bars = reinterpret_cast<ExBars<NS>*>(rg + 1);
+    const int warp = uni(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
     const int npair = gridDim.x >> 1, pair = blockIdx.x >> 1;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < EX_STAGES2; ++s) {
+        for (int s = 0; s < NS; ++s) {
             mbar_init(&bars->full[s], 1);
             mbar_init(&bars->empty[s], 1);
         }
@@ -349,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
     fence_before();
     cluster_sync_all();
     fence_after();
-    const uint32_t tmem = bars->tmem_base;
+    const uint32_t tmem = uni(bars->tmem_base);
     volatile int* abort = &bars->abort;
     bool timed_out = false;
     TileWalk walk{rg, a.E, (a.J + 255) / 256, OP == EX_WGRAD ? 0 : 256, (a.I + 255) / 256};
@@ -358,20 +459,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(EX_REGS_LOW));
         if (warp == 0) {
-            if (lane == 0) {
-                int s = 0;
-                uint32_t ph = 0;
-                for (long long t = pair; !timed_out && walk.seek(t, mb, cb); t += npair) {
-                    const int e = walk.e, r0 = rg->begin[e], rows = rg->end[e] - r0;
-                    const int nk = ex_kblocks<OP, KIND>(a, rows);
-                    const int arow = mb * 256 + (int)rank * 128, brow = cb * 256 + (int)rank * 128;
-                    for (int kb = 0; kb < nk; ++kb) {
-                        if (!mbar_wait(&bars->empty[s], ph ^ 1u, abort)) {
-                            timed_out = true;
-                            break;
-                        }
-                        const uint32_t sa = base + s * EX_STAGE2_BYTES, sb = sa + EX_STAGE2_BYTES / 2;
-                        const uint32_t bar = map_rank(su32(&bars->full[s]), 0);
+            int s = 0;
+            uint32_t ph = 0;
+            for (long long t = pair; !timed_out && uni(walk.seek(t, mb, cb)); t += npair) {
+                const int e = uni(walk.e), r0 = uni(rg->begin[e]), rows = uni(rg->end[e]) - r0;
+                const int nk = ex_kblocks<OP, KIND>(a, rows);
+                const int arow = uni(mb) * 256 + (int)rank * 128, brow = uni(cb) * 256 + (int)rank * 128;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&bars->empty[s], ph ^ 1u, abort))) {
+                        timed_out = true;
+                        break;
+                    }
+                    const uint32_t sa = base + s * EX_STAGE2_BYTES, sb = sa + EX_STAGE2_BYTES / 2;
+                    const uint32_t bar = map_rank(su32(&bars->full[s]), 0);
+                    if (elect_one()) {
                         if (leader) mbar_expect_tx(&bars->full[s], 2 * EX_STAGE2_BYTES);
                         if constexpr (OP == EX_WGRAD) {
                             if (kb * KE + KE <= rows) {
@@ -397,77 +498,88 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
                                     ex_load_3d_pair(sb + b * 8192, &maps.b, bar, brow + 64 * b, kb * KE, e);
                             }
                         }
-                        if (++s == EX_STAGES2) {
-                            s = 0;
-                            ph ^= 1u;
-                        }
                     }
-                }
-                if (timed_out) *abort = 1;
-                // every load this CTA issued completes before it may exit: the leader's MMA commits release
-                // each stage after consuming it (bounded)
-                for (int q = 0; q < EX_STAGES2; ++q) {
-                    mbar_wait(&bars->empty[s], ph ^ 1u, abort, true);
-                    if (++s == EX_STAGES2) {
+                    __syncwarp();
+                    if (++s == NS) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
             }
+            if (timed_out) *abort = 1;
+            // every load this CTA issued completes before it may exit: the leader's MMA commits release
+            // each stage after consuming it (bounded)
+            for (int q = 0; q < NS; ++q) {
+                mbar_wait(&bars->empty[s], ph ^ 1u, abort, true);
+                if (++s == NS) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
         } else if (warp == 1) {
-            if (lane == 0 && leader) {
+            if (leader) {
+                const uint64_t a0 = AMN ? sdesc_mn16(base) : sdesc(base);
+                const uint64_t b0 = BMN ? sdesc_mn16(base + EX_STAGE2_BYTES / 2) : sdesc(base + EX_STAGE2_BYTES / 2);
+                const uint32_t ahi = (uint32_t)(a0 >> 32), bhi = (uint32_t)(b0 >> 32);
+                constexpr uint32_t ASTEP = (AMN ? 2048 : 32) >> 4, BSTEP = (BMN ? 2048 : 32) >> 4;   // one MMA's depth
                 int s = 0;
                 uint32_t ph = 0, part = 0;   // accumulator parts so far: part n uses TMEM buffer n & 1
-                for (long long t = pair; !timed_out && walk.seek(t, mb, cb); t += npair) {
-                    const int nk = ex_kblocks<OP, KIND>(a, rg->end[walk.e] - rg->begin[walk.e]);
+                for (long long t = pair; !timed_out && uni(walk.seek(t, mb, cb)); t += npair) {
+                    const int nk = uni(ex_kblocks<OP, KIND>(a, rg->end[walk.e] - rg->begin[walk.e]));
                     for (int kb = 0; kb < nk; ++kb) {
-                        const int acc = (int)(part & 1u);
-                        if ((kb % PART) == 0 && !mbar_wait(&bars->tempty[acc], ((part >> 1) & 1u) ^ 1u, abort)) {
-                            timed_out = true;
-                            break;
-                        }
-                        if (!mbar_wait(&bars->full[s], ph, abort)) {
+                        const uint32_t acc = part & 1u;
+                        bool ok = true;
+                        if ((kb % PART) == 0) ok = mbar_wait(&bars->tempty[acc], ((part >> 1) & 1u) ^ 1u, abort);
+                        ok = ok && mbar_wait(&bars->full[s], ph, abort);
+                        if (!__all_sync(0xffffffffu, ok)) {
                             timed_out = true;
                             break;
                         }
                         fence_after();
-                        const uint32_t d = tmem + (uint32_t)(acc * 256);
-                        const uint32_t sa = base + s * EX_STAGE2_BYTES, sb = sa + EX_STAGE2_BYTES / 2;
+                        const uint32_t d = tmem + acc * 256u;
+                        const uint32_t alo = (uint32_t)a0 + s * (EX_STAGE2_BYTES >> 4);
+                        const uint32_t blo = (uint32_t)b0 + s * (EX_STAGE2_BYTES >> 4);
+                        const bool last = (kb % PART) == PART - 1 || kb + 1 == nk;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint64_t da = AMN ? sdesc_mn16(sa + k * 2048) : sdesc(sa + k * 32);
-                            const uint64_t db = BMN ? sdesc_mn16(sb + k * 2048) : sdesc(sb + k * 32);
-                            ex_umma<KIND, 2>(d, da, db, id, ((kb % PART) | k) != 0);
+                            for (int k = 0; k < 4; ++k)
+                                ex_umma<KIND, 2>(d, desc64(ahi, alo + k * ASTEP), desc64(bhi, blo + k * BSTEP), id,
+                                                 ((kb % PART) | k) != 0);
+                            umma2_commit_both(&bars->empty[s]);
+                            if (last) umma2_commit_both(&bars->tfull[acc]);
                         }
-                        umma2_commit_both(&bars->empty[s]);
-                        if ((kb % PART) == PART - 1 || kb + 1 == nk) {
-                            umma2_commit_both(&bars->tfull[acc]);
-                            ++part;
-                        }
-                        if (++s == EX_STAGES2) {
+                        __syncwarp();
+                        part += last;
+                        if (++s == NS) {
                             s = 0;
                             ph ^= 1u;
                         }
                     }
                 }
                 if (timed_out) *abort = 1;
-                umma2_commit_both(&bars->drain);
-                mbar_wait(&bars->drain, 0, abort, true);
-            } else if (lane == 0) {
-                mbar_wait(&bars->drain, 0, abort, true);
+                if (elect_one()) umma2_commit_both(&bars->drain);
+                __syncwarp();
             }
+            // the peer has nothing to issue; it waits for the leader's last MMA like the leader itself
+            mbar_wait(&bars->drain, 0, abort, true);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EX_REGS_HIGH));
         const int ew = warp - 4, q = warp & 3, h = ew >> 2;
-        unsigned char* stage = gbase + EX_STAGES2 * EX_STAGE2_BYTES + ew * STAGE_OUT_BYTES;
-        const uint32_t stage_s = base + EX_STAGES2 * EX_STAGE2_BYTES + ew * STAGE_OUT_BYTES;
+        unsigned char* stage = gbase + NS * EX_STAGE2_BYTES + ew * P::NOUT * STAGE_OUT_BYTES;
+        const uint32_t stage_s = base + NS * EX_STAGE2_BYTES + ew * P::NOUT * STAGE_OUT_BYTES;
+        int buf = 0;
         const uint32_t lead_tempty0 = map_rank(su32(&bars->tempty[0]), 0);
         const uint32_t lead_tempty1 = map_rank(su32(&bars->tempty[1]), 0);
         uint32_t part = 0;
         for (long long t = pair; !timed_out && walk.seek(t, mb, cb); t += npair) {
             const int e = walk.e, r0 = rg->begin[e], rows = rg->end[e] - r0;
             const int parts = (ex_kblocks<OP, KIND>(a, rows) + PART - 1) / PART;
+            const int in_tile = mb * 256 + (int)rank * 128 + q * 32, j0 = cb * 256 + h * 128;
+            const int row0 = OP == EX_WGRAD ? in_tile : r0 + in_tile;
+            const int nvalid = (OP == EX_WGRAD ? a.I : rows) - in_tile;
+            EpiRow<4> er;
+            ex_fetch<4, OP, KIND>(er, row0, nvalid, j0, e, a);
             float acc[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -486,12 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
                 if (lane == 0) mbar_arrive_cluster(b ? lead_tempty1 : lead_tempty0);
             }
             if (timed_out) break;
-            const int in_tile = mb * 256 + (int)rank * 128 + q * 32;
-            if constexpr (OP == EX_WGRAD)
-                ex_store<TC, 4, OP, KIND>(acc, in_tile, a.I - in_tile, cb * 256 + h * 128, e, a, &maps.c, stage, stage_s);
-            else
-                ex_store<TC, 4, OP, KIND>(acc, r0 + in_tile, rows - in_tile, cb * 256 + h * 128, e, a, &maps.c, stage,
-                                          stage_s);
+            ex_store<TC, 4, OP, KIND, P::NOUT>(acc, er, row0, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
         }
         if (timed_out) *abort = 1;
         if (lane == 0) bulk_wait_all0();
@@ -507,20 +614,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
 
 // ------------------------------------------------------------------ one SM per tile (forward)
 
-template <int BNT>
-struct ExTile {
-    static constexpr int NS = BNT == 64 ? 8 : 6;
-    static constexpr int STAGE = (128 + BNT) * 128;
-    static constexpr int WC = BNT == 64 ? 64 : BNT / 2;     // columns per epilogue warp
+// BNT: tile columns (weight rows); AR: rows of X a stage holds.
+template <int BNT_, int AR_, int NS_, int WC_>
+struct ExTileT {
+    static constexpr int BNT = BNT_, AR = AR_, NS = NS_;
+    static constexpr int WC = WC_;                             // columns per epilogue warp
+    static constexpr int STAGE = (AR + BNT) * 128;
     static constexpr int TMEM = 2 * BNT;
     static constexpr int SMEM = NS * STAGE + OUT_BYTES + (int)sizeof(Ranges) + (int)sizeof(ExBars<NS>) + 256;
 };
+template <int BNT>
+using ExTile = ExTileT<BNT, 128, BNT == 64 ? 8 : 6, BNT == 64 ? 64 : BNT / 2>;
+// Calls of at most 32 rows: a stage holds 32 rows of X and 32 of W, 24 stages deep, so that each SM has about 96 KB
+// of weights on their way. The MMA still reads 128 rows from a stage's first byte on: rows past the 32 are
+// whatever the next blocks of shared memory hold (the last stage's end in the output buffers) and only reach
+// accumulator rows that are never read.
+using ExFew = ExTileT<32, 32, 24, 32>;
+static_assert((ExFew::NS - 1) * ExFew::STAGE + 128 * 128 <= ExFew::NS * ExFew::STAGE + OUT_BYTES, "128 rows stay inside");
 
-template <typename TC, int KIND, int BNT>
+template <typename TC, int KIND, typename T>
 __global__ void __launch_bounds__(THREADS, 1)
     expert_tile_kernel(const __grid_constant__ ExpertMaps maps, const __grid_constant__ ExpertArgs a, uint32_t id) {
-    using T = ExTile<BNT>;
-    constexpr int NS = T::NS;
+    constexpr int NS = T::NS, BNT = T::BNT, AR = T::AR;
     constexpr int KE = KIND == EX_F8 ? 128 : 64;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = su32(smem_raw);
@@ -528,7 +643,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     unsigned char* gbase = smem_raw + (base - raw);
     Ranges* rg = reinterpret_cast<Ranges*>(gbase + NS * T::STAGE + OUT_BYTES);
     ExBars<NS>* bars = reinterpret_cast<ExBars<NS>*>(rg + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uni(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int nk = ex_kblocks<EX_FWD, KIND>(a, 0);
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -548,87 +663,95 @@ __global__ void __launch_bounds__(THREADS, 1)
                      "r"(T::TMEM));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.b)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.a32)) : "memory");
+    }
     pdl_wait();
     if (warp == 2) read_ranges(a, rg, a.count && blockIdx.x == 0);
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = bars->tmem_base;
+    const uint32_t tmem = uni(bars->tmem_base);
     volatile int* abort = &bars->abort;
     bool timed_out = false;
     TileWalk walk{rg, a.E, (a.J + BNT - 1) / BNT, 128, 0};
     int mb, cb;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            for (long long t = blockIdx.x; !timed_out && walk.seek(t, mb, cb); t += gridDim.x) {
-                const int e = walk.e, row = rg->begin[e] + mb * 128;
-                const bool few = rg->end[e] - row <= 32;
-                const uint32_t tx = (uint32_t)((few ? 32 : 128) + BNT) * 128u;
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait(&bars->empty[s], ph ^ 1u, abort)) {
-                        timed_out = true;
-                        break;
-                    }
-                    const uint32_t sa = base + s * T::STAGE;
-                    mbar_expect_tx(&bars->full[s], tx);
-                    tma_load_2d(sa, few ? &maps.a32 : &maps.a, &bars->full[s], kb * KE, row);
-                    ex_load_3d(sa + 128 * 128, &maps.b, &bars->full[s], kb * KE, cb * BNT, e);
-                    if (++s == NS) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+        int s = 0;
+        uint32_t ph = 0;
+        for (long long t = blockIdx.x; !timed_out && uni(walk.seek(t, mb, cb)); t += gridDim.x) {
+            const int e = uni(walk.e), row = uni(rg->begin[e] + mb * 128), col = uni(cb) * BNT;
+            const bool few = AR == 32 || uni(rg->end[e]) - row <= 32;
+            const uint32_t tx = (uint32_t)((few ? 32 : 128) + BNT) * 128u;
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->empty[s], ph ^ 1u, abort))) {
+                    timed_out = true;
+                    break;
                 }
-            }
-            if (timed_out) *abort = 1;
-            // drain, also when another role gave up: every stage whose load may still be in flight completes its
-            // full phase before the CTA may exit (a stage never loaded, or already consumed, passes at once)
-            for (int q = 0; q < NS; ++q) {
-                if (--s < 0) {
-                    s = NS - 1;
+                const uint32_t sa = base + s * T::STAGE;
+                if (elect_one()) {
+                    mbar_expect_tx(&bars->full[s], tx);
+                    if (few) tma_load_2d(sa, &maps.a32, &bars->full[s], kb * KE, row);
+                    else tma_load_2d(sa, &maps.a, &bars->full[s], kb * KE, row);
+                    ex_load_3d(sa + AR * 128, &maps.b, &bars->full[s], kb * KE, col, e);
+                }
+                __syncwarp();
+                if (++s == NS) {
+                    s = 0;
                     ph ^= 1u;
                 }
-                mbar_wait(&bars->full[s], ph, abort, true);
             }
+        }
+        if (timed_out) *abort = 1;
+        // drain, also when another role gave up: every stage whose load may still be in flight completes its
+        // full phase before the CTA may exit (a stage never loaded, or already consumed, passes at once)
+        for (int q = 0; q < NS; ++q) {
+            if (--s < 0) {
+                s = NS - 1;
+                ph ^= 1u;
+            }
+            mbar_wait(&bars->full[s], ph, abort, true);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0, part = 0;
-            for (long long t = blockIdx.x; !timed_out && walk.seek(t, mb, cb); t += gridDim.x) {
-                for (int kb = 0; kb < nk; ++kb) {
-                    const int acc = (int)(part & 1u);
-                    if ((kb % PART) == 0 && !mbar_wait(&bars->tempty[acc], ((part >> 1) & 1u) ^ 1u, abort)) {
-                        timed_out = true;
-                        break;
-                    }
-                    if (!mbar_wait(&bars->full[s], ph, abort)) {
-                        timed_out = true;
-                        break;
-                    }
-                    fence_after();
-                    const uint32_t d = tmem + (uint32_t)(acc * BNT);
-                    const uint32_t sa = base + s * T::STAGE, sb = sa + 128 * 128;
+        const uint64_t a0 = sdesc(base), b0 = sdesc(base + AR * 128);
+        const uint32_t ahi = (uint32_t)(a0 >> 32), bhi = (uint32_t)(b0 >> 32);
+        int s = 0;
+        uint32_t ph = 0, part = 0;
+        for (long long t = blockIdx.x; !timed_out && uni(walk.seek(t, mb, cb)); t += gridDim.x) {
+            for (int kb = 0; kb < nk; ++kb) {
+                const uint32_t acc = part & 1u;
+                bool ok = true;
+                if ((kb % PART) == 0) ok = mbar_wait(&bars->tempty[acc], ((part >> 1) & 1u) ^ 1u, abort);
+                ok = ok && mbar_wait(&bars->full[s], ph, abort);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    timed_out = true;
+                    break;
+                }
+                fence_after();
+                const uint32_t d = tmem + acc * BNT;
+                const uint32_t alo = (uint32_t)a0 + s * (T::STAGE >> 4), blo = (uint32_t)b0 + s * (T::STAGE >> 4);
+                const bool last = (kb % PART) == PART - 1 || kb + 1 == nk;
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        ex_umma<KIND, 1>(d, sdesc(sa + k * 32), sdesc(sb + k * 32), id, ((kb % PART) | k) != 0);
+                        ex_umma<KIND, 1>(d, desc64(ahi, alo + 2 * k), desc64(bhi, blo + 2 * k), id, ((kb % PART) | k) != 0);
                     umma_commit(&bars->empty[s]);
-                    if ((kb % PART) == PART - 1 || kb + 1 == nk) {
-                        umma_commit(&bars->tfull[acc]);
-                        ++part;
-                    }
-                    if (++s == NS) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                    if (last) umma_commit(&bars->tfull[acc]);
+                }
+                __syncwarp();
+                part += last;
+                if (++s == NS) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            if (timed_out) *abort = 1;
-            umma_commit(&bars->drain);
-            mbar_wait(&bars->drain, 0, abort, true);
         }
+        if (timed_out) *abort = 1;
+        if (elect_one()) umma_commit(&bars->drain);
+        __syncwarp();
+        mbar_wait(&bars->drain, 0, abort, true);
     } else {
         constexpr int NC = T::WC / 32;
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
@@ -637,9 +760,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t stage_s = base + NS * T::STAGE + ew * STAGE_OUT_BYTES;
         const int parts = (nk + PART - 1) / PART;
         uint32_t part = 0;
+        int buf = 0;
         for (long long t = blockIdx.x; !timed_out && walk.seek(t, mb, cb); t += gridDim.x) {
             const int e = walk.e, row = rg->begin[e] + mb * 128 + q * 32;
             const bool some = active && row < rg->end[e];
+            const int nvalid = active ? rg->end[e] - row : 0, j0 = cb * BNT + h * T::WC;
+            EpiRow<NC> er;
+            ex_fetch<NC, EX_FWD, KIND>(er, row, nvalid, j0, e, a);
             float acc[NC][32];
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -658,9 +785,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(&bars->tempty[b]);
             }
             if (timed_out) break;
-            if (some)
-                ex_store<TC, NC, EX_FWD, KIND>(acc, row, rg->end[e] - row, cb * BNT + h * T::WC, e, a, &maps.c, stage,
-                                               stage_s);
+            if (some) {
+                if constexpr (AR == 32) ex_store_few<TC, KIND>(acc[0], er, row, nvalid, j0, a);
+                else ex_store<TC, NC, EX_FWD, KIND, 1>(acc, er, row, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
+            }
         }
         if (timed_out) *abort = 1;
         if (lane == 0) bulk_wait_all0();
@@ -674,9 +802,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-constexpr int EX_SMEM2 =
-    EX_STAGES2 * EX_STAGE2_BYTES + OUT_BYTES + (int)sizeof(Ranges) + (int)sizeof(ExBars<EX_STAGES2>) + 256;
-static_assert(EX_SMEM2 <= 227 * 1024 && ExTile<64>::SMEM <= 227 * 1024 && ExTile<128>::SMEM <= 227 * 1024, "shared memory");
+template <int KIND>
+constexpr int EX_SMEM2 = ExPair<KIND>::NS * EX_STAGE2_BYTES + ExPair<KIND>::OUT + (int)sizeof(Ranges) +
+                         (int)sizeof(ExBars<ExPair<KIND>::NS>) + 256;
+static_assert(EX_SMEM2<EX_F16> <= 227 * 1024 && EX_SMEM2<EX_F8> <= 227 * 1024, "shared memory");
+static_assert(ExTile<64>::SMEM <= 227 * 1024 && ExTile<128>::SMEM <= 227 * 1024 && ExFew::SMEM <= 227 * 1024, "shared memory");
 
 // ------------------------------------------------------------------ backward: dP, bias sums, padded last blocks
 
@@ -824,12 +954,13 @@ __global__ void __launch_bounds__(256) expert_prep_kernel(const __grid_constant_
     }
 }
 
-// db[e][n] = sum over the expert's chunks, in order.
+// db[e][n] = sum over the expert's chunks: 32 columns a block, eight contiguous shares of the chunks added in order.
 __global__ void __launch_bounds__(256) expert_bias_kernel(const __grid_constant__ ExpertArgs a, int N,
                                                           const float* __restrict__ part, float* __restrict__ db) {
     pdl_wait();
     __shared__ Ranges rg;
     __shared__ long long first;
+    __shared__ float share[8][33];
     const int e = blockIdx.y;
     if (threadIdx.x < 32) {
         read_ranges(a, &rg, false);
@@ -841,14 +972,25 @@ __global__ void __launch_bounds__(256) expert_bias_kernel(const __grid_constant_
         if (threadIdx.x == 0) first = s;
     }
     __syncthreads();
-    const int n = blockIdx.x * blockDim.x + threadIdx.x;
-    if (n >= N) return;
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int n = blockIdx.x * 32 + lane;
     const int chunks = (rg.end[e] - rg.begin[e] + PREP_ROWS - 1) / PREP_ROWS;
-    const float* p = part + first * N + n;
+    const int per = (chunks + 7) / 8;
+    const int j0 = g * per, j1 = j0 + per < chunks ? j0 + per : chunks;
     float s = 0.f;
+    if (n < N) {
+        const float* p = part + first * N + n;
 #pragma unroll 8
-    for (int j = 0; j < chunks; ++j) s += p[(long long)j * N];
-    db[(long long)e * N + n] = s;
+        for (int j = j0; j < j1; ++j) s += p[(long long)j * N];
+    }
+    share[g][lane] = s;
+    __syncthreads();
+    if (g == 0 && n < N) {
+        s = share[0][lane];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) s += share[q][lane];
+        db[(long long)e * N + n] = s;
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -874,28 +1016,30 @@ bool ex_map(CUtensorMap* m, const void* p, int es, dlrm_dtype dt, int rank, long
 
 int ex_size(dlrm_dtype dt) { return dt == DLRM_F32 ? 4 : dt == DLRM_E4M3 ? 1 : 2; }
 
-template <typename TC, int OP, int KIND>
-dlrm_status launch_pair(const ExpertMaps& maps, const ExpertArgs& a, uint32_t id, long long tiles, cudaStream_t st) {
-    auto kern = expert_pair_kernel<TC, OP, KIND>;
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, EX_SMEM2);
-    const int pairs = device_sms() / 2;
-    const dim3 grid((unsigned)(2 * std::min<long long>(tiles, pairs)));
-    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(EX_THREADS2), (size_t)EX_SMEM2, st, maps, a, id));
-    return DLRM_OK;
-}
-
-template <typename TC, int KIND, int BNT>
-dlrm_status launch_tile(const ExpertMaps& maps, const ExpertArgs& a, uint32_t id, long long tiles, cudaStream_t st) {
-    auto kern = expert_tile_kernel<TC, KIND, BNT>;
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ExTile<BNT>::SMEM);
-    const dim3 grid((unsigned)std::min<long long>(tiles, device_sms()));
-    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(THREADS), (size_t)ExTile<BNT>::SMEM, st, maps, a, id));
-    return DLRM_OK;
-}
-
 // Most tiles a call can have: row blocks of every expert, the experts with rows being at most min(E, M).
 long long most_tiles(int E, long long M, int rows_per, long long nb) {
     return (M / rows_per + std::min<long long>(E, M)) * nb;
+}
+
+template <typename TC, int OP, int KIND>
+dlrm_status launch_pair(const ExpertMaps& maps, const ExpertArgs& a, uint32_t id, long long tiles, cudaStream_t st) {
+    auto kern = expert_pair_kernel<TC, OP, KIND>;
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, EX_SMEM2<KIND>);
+    const int pairs = device_sms() / 2;
+    const dim3 grid((unsigned)(2 * std::min<long long>(tiles, pairs)));
+    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(EX_THREADS2), (size_t)EX_SMEM2<KIND>, st, maps, a, id));
+    return DLRM_OK;
+}
+
+template <typename TC, int KIND, typename T>
+dlrm_status launch_tile(const ExpertMaps& maps, const ExpertArgs& a, int fmt, cudaStream_t st) {
+    auto kern = expert_tile_kernel<TC, KIND, T>;
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    const long long tiles = most_tiles(a.E, a.M, 128, (a.J + T::BNT - 1) / T::BNT);
+    const dim3 grid((unsigned)std::min<long long>(tiles, device_sms()));
+    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(THREADS), (size_t)T::SMEM, st, maps, a,
+                              ex_idesc(fmt, false, false, 128, T::BNT)));
+    return DLRM_OK;
 }
 
 }  // namespace
@@ -909,24 +1053,24 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
     const int es = ex_size(dt), ke = 128 / es;
     ExpertArgs a{E, M, N, 0, K, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, err};
     // SM pairs once their 256 x 256 tiles can fill them (rows spread evenly over the experts); otherwise one SM
-    // per tile, 128 columns wide, or 64 when that leaves SMs without a tile
-    const long long nb2 = (N + 255) / 256;
-    const bool pair = ((long long)M / 256) * nb2 >= device_sms() / 2;
-    const long long rb = (M + 127) / 128 > std::min(E, M) ? (M + 127) / 128 : std::min(E, M);
-    const int bnt = rb * ((N + 127) / 128) >= device_sms() ? 128 : 64;
+    // per tile, of the width whose last round over the SMs wastes least
+    const long long nb2 = (N + 255) / 256, sms = device_sms();
+    const bool few = M <= 32 && EX_FEWW == 32, pair = !few && ((long long)M / 256) * nb2 >= sms / 2;
+    const long long rb = std::max<long long>((M + 127) / 128, std::min(E, M));
+    auto rounds = [&](int w) { return (rb * ((N + w - 1) / w) + sms - 1) / sms * w; };
+    const int bnt = few ? 32 : M <= 32 ? EX_FEWW : rounds(128) <= rounds(64) ? 128 : 64;
     ExpertMaps maps{};
     if (!ex_map(&maps.a, X, es, dt, 2, K, M, 1, ldx, ke, 128) || !ex_map(&maps.a32, X, es, dt, 2, K, M, 1, ldx, ke, 32) ||
         !ex_map(&maps.b, W, es, dt, 3, K, N, E, ldw, ke, pair ? 128 : bnt) ||
         !ex_map(&maps.c, Y, ex_size(y_dt), y_dt, 2, N, M, 1, ldy, 128 / ex_size(y_dt), 32))
         return DLRM_ERR_CUDA;
     const int fmt = dt == DLRM_BF16 ? 1 : 0;
-#define DLRM_EX_FWD(TC, KIND)                                                                                           \
-    return pair ? launch_pair<TC, EX_FWD, KIND>(maps, a, ex_idesc(fmt, false, false, 256, 256), most_tiles(E, M, 256, nb2), st) \
-           : bnt == 128                                                                                                 \
-               ? launch_tile<TC, KIND, 128>(maps, a, ex_idesc(fmt, false, false, 128, 128),                             \
-                                            most_tiles(E, M, 128, (N + 127) / 128), st)                                 \
-               : launch_tile<TC, KIND, 64>(maps, a, ex_idesc(fmt, false, false, 128, 64),                               \
-                                           most_tiles(E, M, 128, (N + 63) / 64), st);
+#define DLRM_EX_FWD(TC, KIND)                                                                                    \
+    return pair ? launch_pair<TC, EX_FWD, KIND>(maps, a, ex_idesc(fmt, false, false, 256, 256),                  \
+                                                most_tiles(E, M, 256, nb2), st)                                  \
+           : few        ? launch_tile<TC, KIND, ExFew>(maps, a, fmt, st)                                         \
+           : bnt == 128 ? launch_tile<TC, KIND, ExTile<128>>(maps, a, fmt, st)                                   \
+                        : launch_tile<TC, KIND, ExTile<64>>(maps, a, fmt, st);
     if (dt == DLRM_E4M3) {
         if (y_dt == DLRM_F32) DLRM_EX_FWD(float, EX_F8)
         if (y_dt == DLRM_BF16) DLRM_EX_FWD(__nv_bfloat16, EX_F8)
@@ -994,7 +1138,7 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
         base.count = false;
     }
     if (db) {
-        DLRM_PDL_CHECK(launch_pdl(expert_bias_kernel, dim3((N + 255) / 256, E), dim3(256), 0, st, base, N,
+        DLRM_PDL_CHECK(launch_pdl(expert_bias_kernel, dim3((N + 31) / 32, E), dim3(256), 0, st, base, N,
                                   (const float*)part, db));
     }
     const int fmt = dt == DLRM_BF16 ? 1 : 0;

@@ -11,12 +11,15 @@
 //   1. (id, position) pairs are sorted by id, stably: one block's bitonic
 //      sort in shared memory for short calls, else an LSD radix sort whose
 //      digits are as wide as the table needs (two passes up to 2^20 rows).
+//      The sort takes few SMs and little bandwidth, so the other blocks of
+//      its launches write the table's zeros meanwhile; rows with lookups are
+//      written again by the next steps.
 //   2. The sorted pairs are cut into windows of fixed length, each summed by
 //      one group of threads per column slice, whatever rows they belong to, so
 //      a row looked up thousands of times costs no more per lookup than any
 //      other. A run of equal ids inside a window is final and goes straight to
 //      its row; the parts of a run that crosses windows go to a partial
-//      buffer. The same launch writes zeros to the rows nothing looked up.
+//      buffer.
 //   3. The partial sums of the crossing runs are added in window order.
 #include <algorithm>
 
@@ -133,14 +136,42 @@ constexpr int RS_ITEMS = 8;            // keys per thread and tile
 constexpr int RS_TILE = RS_THREADS * RS_ITEMS;
 constexpr int RS_BLOCKS_MAX = 296;
 
+// A share of the table's bytes, zeroed by the blocks of a sorting launch that do not sort.
+struct Zeros {
+    char* base;
+    long long begin, end;     // bytes
+    int sorters;              // blocks of the launch that sort
+};
+__device__ __forceinline__ void write_zeros(const Zeros& z) {
+    const long long nb = gridDim.x - z.sorters, b = (long long)blockIdx.x - z.sorters;
+    // 16-byte stores from the first aligned address of the share; its ragged ends byte by byte
+    char* p0 = z.base + z.begin;
+    char* p1 = z.base + z.end;
+    char* q0 = reinterpret_cast<char*>(((uintptr_t)p0 + 15) & ~(uintptr_t)15);
+    if (q0 > p1) q0 = p1;
+    char* q1 = q0 + ((p1 - q0) & ~(long long)15);
+    const long long n16 = (q1 - q0) / 16;
+    for (long long i = b * blockDim.x + threadIdx.x; i < n16; i += nb * blockDim.x)
+        reinterpret_cast<uint4*>(q0)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (b == 0) {
+        if ((long long)threadIdx.x < q0 - p0) p0[threadIdx.x] = 0;
+        if ((long long)threadIdx.x < p1 - q1) q1[threadIdx.x] = 0;
+    }
+}
+
 // The whole sort in one block: bitonic over 64-bit words (id, position), which are all different, so the
 // order is that of a stable sort by id. Indices outside the table get id m and end up last.
 __global__ void __launch_bounds__(1024) sort_one_block_kernel(int n, int padded, long long m,
                                                               const int32_t* __restrict__ idx,
                                                               uint32_t* __restrict__ keys,
-                                                              uint32_t* __restrict__ vals, ErrRecord* err) {
+                                                              uint32_t* __restrict__ vals, ErrRecord* err,
+                                                              const __grid_constant__ Zeros zeros) {
     pdl_wait();
     extern __shared__ unsigned long long pairs[];
+    if (blockIdx.x > 0) {
+        write_zeros(zeros);
+        return;
+    }
     unsigned bad = 0;
     for (int i = threadIdx.x; i < padded; i += blockDim.x) {
         unsigned long long p = ~0ull;
@@ -188,9 +219,14 @@ __device__ __forceinline__ uint32_t pass_key(const void* in, long long i, long l
 template <bool FIRST>
 __global__ void __launch_bounds__(RS_THREADS) rs_hist_kernel(long long n, long long m, const void* __restrict__ in,
                                                              int shift, int bits, long long chunk,
-                                                             int* __restrict__ hist, ErrRecord* err) {
+                                                             int* __restrict__ hist, ErrRecord* err,
+                                                             const __grid_constant__ Zeros zeros) {
     pdl_wait();
     __shared__ int h[1 << DIG_BITS_MAX];
+    if ((int)blockIdx.x >= zeros.sorters) {
+        write_zeros(zeros);
+        return;
+    }
     const int radix = 1 << bits;
     for (int i = threadIdx.x; i < radix; i += blockDim.x) h[i] = 0;
     __syncthreads();
@@ -216,8 +252,13 @@ __global__ void __launch_bounds__(RS_THREADS) rs_scatter_kernel(long long n, lon
                                                                 const uint32_t* __restrict__ vin, int shift, int bits,
                                                                 long long chunk, const int* __restrict__ hist,
                                                                 uint32_t* __restrict__ kout,
-                                                                uint32_t* __restrict__ vout) {
+                                                                uint32_t* __restrict__ vout,
+                                                                const __grid_constant__ Zeros zeros) {
     pdl_wait();
+    if ((int)blockIdx.x >= zeros.sorters) {
+        write_zeros(zeros);
+        return;
+    }
     constexpr int W = RS_THREADS / 32;
     constexpr int RMAX = 1 << DIG_BITS_MAX;
     constexpr int PER = RMAX / RS_THREADS;     // digits per thread: consecutive
@@ -226,18 +267,49 @@ __global__ void __launch_bounds__(RS_THREADS) rs_scatter_kernel(long long n, lon
     __shared__ int wsum[W];
     const int radix = 1 << bits;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // totals and prefixes over blocks, coalesced over digits
+    const long long b0 = (long long)blockIdx.x * chunk, b1 = b0 + chunk < n ? b0 + chunk : n;
+    // warp w takes a tile's keys [w, w + 1) * 32 * RS_ITEMS, 32 at a time in order; the first tile's are on their
+    // way while the positions are worked out
+    uint32_t key[RS_ITEMS], val[RS_ITEMS];
+    auto load_tile = [&](long long t0) {
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e) {
+            const long long i = t0 + warp * (32 * RS_ITEMS) + e * 32 + lane;
+            const bool valid = i < b1;
+            key[e] = valid ? pass_key<FIRST>(in, i, m) : 0u;
+            val[e] = valid ? (FIRST ? (uint32_t)i : vin[i]) : 0u;
+        }
+    };
+    load_tile(b0);
+    // totals and prefixes over blocks: each thread takes four neighbouring digits, and the threads left over share
+    // the blocks' rows between them
+    int* tot = reinterpret_cast<int*>(wcount);           // [groups][radix]: 1,024 sums in all
+    int* bef = tot + 4 * RS_THREADS;
+    const int per_group = radix / 4, groups = RS_THREADS / per_group;
+    {
+        const int g = threadIdx.x / per_group, d4 = threadIdx.x - g * per_group;
+        const int nb = zeros.sorters, mine = (nb + groups - 1) / groups;
+        const int q0 = g * mine, q1 = q0 + mine < nb ? q0 + mine : nb;
+        int4 all = make_int4(0, 0, 0, 0), before = all;
+        const int4* row = reinterpret_cast<const int4*>(hist) + d4;
+#pragma unroll 16
+        for (int q = q0; q < q1; ++q) {
+            const int4 v = __ldg(row + (long long)q * per_group);
+            all.x += v.x, all.y += v.y, all.z += v.z, all.w += v.w;
+            if (q < (int)blockIdx.x) before.x += v.x, before.y += v.y, before.z += v.z, before.w += v.w;
+        }
+        reinterpret_cast<int4*>(tot)[threadIdx.x] = all;
+        reinterpret_cast<int4*>(bef)[threadIdx.x] = before;
+    }
+    __syncthreads();
     for (int dg = threadIdx.x; dg < radix; dg += RS_THREADS) {
-        int before = 0, all = 0;
-#pragma unroll 8
-        for (int b = 0; b < (int)gridDim.x; ++b) {
-            const int v = hist[(long long)b * radix + dg];
-            all += v;
-            if (b < (int)blockIdx.x) before += v;
+        int all = 0, before = 0;
+        for (int g = 0; g < groups; ++g) {
+            all += tot[g * radix + dg];
+            before += bef[g * radix + dg];
         }
         next[dg] = all;
-        // kept aside until the scan over digits is known
-        reinterpret_cast<int*>(wcount)[dg] = before;
+        bef[dg] = before;      // only this thread reads or writes column dg
     }
     for (int dg = radix + threadIdx.x; dg < RMAX; dg += RS_THREADS) next[dg] = 0;
     __syncthreads();
@@ -261,27 +333,19 @@ __global__ void __launch_bounds__(RS_THREADS) rs_scatter_kernel(long long n, lon
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const int dg = threadIdx.x * PER + e;
-            if (dg < radix) next[dg] = base + reinterpret_cast<int*>(wcount)[dg];
+            if (dg < radix) next[dg] = base + bef[dg];
             base += v[e];
         }
     }
     __syncthreads();
-    const long long b0 = (long long)blockIdx.x * chunk, b1 = b0 + chunk < n ? b0 + chunk : n;
     const unsigned lt = (1u << lane) - 1u;
     for (long long t0 = b0; t0 < b1; t0 += RS_TILE) {
-        for (int i = threadIdx.x; i < W * RMAX / 2; i += RS_THREADS) reinterpret_cast<uint32_t*>(wcount)[i] = 0;
+        for (int i = threadIdx.x; i < W * per_group * 2; i += RS_THREADS)
+            reinterpret_cast<uint32_t*>(wcount[i / (per_group * 2)])[i % (per_group * 2)] = 0;
         __syncthreads();
-        // warp w takes the tile's keys [w, w + 1) * 32 * RS_ITEMS, 32 at a time in order
+        if (t0 > b0) load_tile(t0);
         const long long w0 = t0 + (long long)warp * (32 * RS_ITEMS);
-        uint32_t key[RS_ITEMS], val[RS_ITEMS];
         int rank[RS_ITEMS];
-#pragma unroll
-        for (int e = 0; e < RS_ITEMS; ++e) {
-            const long long i = w0 + e * 32 + lane;
-            const bool valid = i < b1;
-            key[e] = valid ? pass_key<FIRST>(in, i, m) : 0u;
-            val[e] = valid ? (FIRST ? (uint32_t)i : vin[i]) : 0u;
-        }
 #pragma unroll
         for (int e = 0; e < RS_ITEMS; ++e) {
             const bool valid = w0 + e * 32 + lane < b1;
@@ -332,7 +396,6 @@ struct SumArgs {
     int d;
     long long windows;
     int P;                    // sorted pairs per window
-    int wblocks;              // blocks of this launch that take windows; the others write zero rows
     int slices;               // column slices
     const uint32_t* keys;
     const uint32_t* vals;
@@ -364,35 +427,6 @@ template <typename TI, typename TO, int VEC>
 __global__ void __launch_bounds__(128) run_sum_kernel(const __grid_constant__ SumArgs a) {
     pdl_wait();
     TO* dT = static_cast<TO*>(a.dT);
-    if ((int)blockIdx.x >= a.wblocks) {
-        // zero rows: each warp takes 32 consecutive rows and finds which of them have no pair
-        const int tid = threadIdx.y * blockDim.x + threadIdx.x, lane = tid & 31;
-        const long long nw = (long long)(gridDim.x - a.wblocks) * 4;
-        for (long long g = (long long)(blockIdx.x - a.wblocks) * 4 + (tid >> 5); g * 32 < a.m; g += nw) {
-            const long long r0 = g * 32;
-            const long long lo = warp_lower_bound(a.keys, a.n, r0, lane);
-            const long long hi = lo + warp_lower_bound(a.keys + lo, a.n - lo, r0 + 32, lane);
-            // lane l: is row r0 + l among keys[lo, hi)?
-            long long x = lo, y = hi;
-            const long long mine = r0 + lane;
-            while (x < y) {
-                const long long mid = (x + y) >> 1;
-                if ((long long)a.keys[mid] < mine) x = mid + 1;
-                else y = mid;
-            }
-            const bool there = x < hi && (long long)a.keys[x] == mine;
-            unsigned empty = __ballot_sync(0xffffffffu, !there && mine < a.m);
-            RowRaw<TO, VEC> z;
-            z.zero();
-            while (empty) {
-                const int l = __ffs(empty) - 1;
-                empty &= empty - 1;
-                TO* p = dT + (r0 + l) * a.d;
-                for (int c = lane * VEC; c < a.d; c += 32 * VEC) z.store(p + c);
-            }
-        }
-        return;
-    }
     const long long wb = blockIdx.x / a.slices;
     const int slice = (int)(blockIdx.x - wb * a.slices);
     const long long w = wb * blockDim.y + threadIdx.y;
@@ -450,44 +484,93 @@ __global__ void __launch_bounds__(128) run_sum_kernel(const __grid_constant__ Su
     }
 }
 
+// Adds partial[w + j][0] for j in [j0, j1) to s, in order, eight loads in flight.
+template <int VEC>
+__device__ __forceinline__ void add_parts(const SumArgs& a, long long w, long long j0, long long j1, int c, float (&s)[VEC]) {
+    constexpr int U = 8;
+    for (long long j = j0; j < j1; j += U) {
+        RowRaw<float, VEC> r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (j + u < j1) r[u].load(a.partial + (w + j + u) * 2 * a.d + c);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (j + u < j1) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s[e] += r[u].e[e];
+            }
+    }
+}
+
 // A run that starts inside window w and goes on into w + 1: its parts are partial[w][1], partial[w + 1][0],
-// ... up to the window where it ends. blockDim = (32, 8): 32 columns, eight contiguous shares of the
-// windows, added in order.
-template <typename TO>
+// ... up to the window where it ends. blockDim = (32, 8): each warp looks at one window and adds up a run of few
+// parts by itself, VEC columns a lane; the block's warps share each longer run in eight contiguous pieces, added
+// in order. Which of the two depends on the run's length alone.
+constexpr int JOIN_SHORT = 32;
+template <typename TO, int VEC>
 __global__ void __launch_bounds__(256) run_join_kernel(const __grid_constant__ SumArgs a) {
     pdl_wait();
-    __shared__ float part[8][33];
-    __shared__ long long last_s;
-    const long long w = blockIdx.x;
-    const long long i1 = (w + 1) * a.P;
-    if (i1 >= a.n) return;
-    const uint32_t key = a.keys[i1 - 1];
-    if (key != a.keys[i1] || key == (uint32_t)a.m) return;                    // nothing leaves this window
-    const long long i0 = w * a.P;
-    if (a.keys[i0] == key && i0 > 0 && a.keys[i0 - 1] == key) return;          // it started earlier
-    if (threadIdx.y == 0) {
-        const long long end = i1 + warp_lower_bound(a.keys + i1, a.n - i1, (long long)key + 1, threadIdx.x);
-        if (threadIdx.x == 0) last_s = (end - 1) / a.P;
+    __shared__ float part[8][32][VEC + 1];
+    __shared__ long long parts_of[8];            // parts after the first of each warp's run (0: none, or done)
+    __shared__ uint32_t key_of[8];
+    const long long w0 = (long long)blockIdx.x * 8, w = w0 + threadIdx.y;
+    const int c = (blockIdx.y * 32 + threadIdx.x) * VEC;
+    const long long i0 = w * a.P, i1 = i0 + a.P;
+    long long cnt = 0;
+    uint32_t key = 0;
+    if (i1 < a.n) {
+        key = a.keys[i1 - 1];
+        const uint32_t next = a.keys[i1], first = a.keys[i0], prev = i0 > 0 ? a.keys[i0 - 1] : ~key;
+        // it leaves this window, and did not start before it
+        if (key == next && key != (uint32_t)a.m && !(first == key && prev == key)) {
+            const long long end = i1 + warp_lower_bound(a.keys + i1, a.n - i1, (long long)key + 1, threadIdx.x);
+            cnt = (end - 1) / a.P - w;
+        }
+    }
+    float s[VEC];
+    auto first_part = [&](long long win) {
+        RowRaw<float, VEC> r;
+        r.load(a.partial + (win * 2 + 1) * a.d + c);
+        r.get(s);
+    };
+    auto write = [&](uint32_t k) {
+        TO* p = static_cast<TO*>(a.dT) + (long long)k * a.d + c;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) p[e] = Cvt<TO>::from_f(s[e] * a.scale);
+    };
+    if (cnt > 0 && cnt <= JOIN_SHORT) {
+        if (c < a.d) {
+            first_part(w);
+            add_parts<VEC>(a, w, 1, cnt + 1, c, s);
+            write(key);
+        }
+        cnt = 0;
+    }
+    if (threadIdx.x == 0) {
+        parts_of[threadIdx.y] = cnt;
+        key_of[threadIdx.y] = key;
     }
     __syncthreads();
-    const long long cnt = last_s - w;            // windows after w that hold a part
-    const long long per = (cnt + 7) / 8;
-    const long long j0 = 1 + threadIdx.y * per, j1 = j0 + per < cnt + 1 ? j0 + per : cnt + 1;
-    for (int c0 = 0; c0 < a.d; c0 += 32) {
-        const int c = c0 + threadIdx.x;
-        float s = 0.f;
+    for (int q = 0; q < 8; ++q) {
+        const long long n = parts_of[q];
+        if (n == 0) continue;                    // the same for the whole block
+        const long long per = (n + 7) / 8;
+        const long long j0 = 1 + threadIdx.y * per, j1 = j0 + per < n + 1 ? j0 + per : n + 1;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s[e] = 0.f;
         if (c < a.d) {
-            if (threadIdx.y == 0) s = a.partial[(w * 2 + 1) * a.d + c];
-#pragma unroll 8
-            for (long long j = j0; j < j1; ++j) s += a.partial[(w + j) * 2 * a.d + c];
+            if (threadIdx.y == 0) first_part(w0 + q);
+            add_parts<VEC>(a, w0 + q, j0, j1, c, s);
         }
-        part[threadIdx.y][threadIdx.x] = s;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) part[threadIdx.y][threadIdx.x][e] = s[e];
         __syncthreads();
         if (threadIdx.y == 0 && c < a.d) {
-            s = part[0][threadIdx.x];
 #pragma unroll
-            for (int q = 1; q < 8; ++q) s += part[q][threadIdx.x];
-            static_cast<TO*>(a.dT)[(long long)key * a.d + c] = Cvt<TO>::from_f(s * a.scale);
+            for (int g = 1; g < 8; ++g)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s[e] += part[g][threadIdx.x][e];
+            write(key_of[q]);
         }
         __syncthreads();
     }
@@ -502,14 +585,17 @@ dlrm_status sum_vec(SumArgs a, cudaStream_t st) {
     const int tx = pow2_at_least(runs, 128);
     const dim3 block(tx, 128 / tx);
     a.slices = (runs + tx - 1) / tx;
-    const long long wblocks = (a.windows + block.y - 1) / block.y * a.slices;
-    // zero rows: a warp per 32 rows, up to eight blocks per SM
-    const long long zblocks = std::min<long long>((a.m + 127) / 128, 8ll * device_sms());
-    if (wblocks + zblocks > (1ll << 31) - 1) return DLRM_ERR_UNSUPPORTED;
-    a.wblocks = (int)wblocks;
-    DLRM_PDL_CHECK(launch_pdl(run_sum_kernel<TI, TO, VEC>, dim3((unsigned)(wblocks + zblocks)), block, 0, st, a));
-    if (a.windows > 1)
-        DLRM_PDL_CHECK(launch_pdl(run_join_kernel<TO>, dim3((unsigned)(a.windows - 1)), dim3(32, 8), 0, st, a));
+    const long long blocks = (a.windows + block.y - 1) / block.y * a.slices;
+    if (blocks > (1ll << 31) - 1) return DLRM_ERR_UNSUPPORTED;
+    if (blocks == 0) return DLRM_OK;
+    DLRM_PDL_CHECK(launch_pdl(run_sum_kernel<TI, TO, VEC>, dim3((unsigned)blocks), block, 0, st, a));
+    if (a.windows > 1) {
+        const unsigned nw = (unsigned)((a.windows - 1 + 7) / 8);
+        if (a.d % 4 == 0)
+            DLRM_PDL_CHECK(launch_pdl(run_join_kernel<TO, 4>, dim3(nw, (a.d + 127) / 128), dim3(32, 8), 0, st, a));
+        else
+            DLRM_PDL_CHECK(launch_pdl(run_join_kernel<TO, 1>, dim3(nw, (a.d + 31) / 32), dim3(32, 8), 0, st, a));
+    }
     return DLRM_OK;
 }
 
@@ -544,7 +630,7 @@ GradLayout grad_layout(long long m, int d, long long n) {
     int kb = 1;
     while ((1ll << kb) <= m) ++kb;             // ids 0 .. m
     L.passes = n <= SORT1_MAX ? 0 : (kb + DIG_BITS_MAX - 1) / DIG_BITS_MAX;
-    L.bits = L.passes ? (kb + L.passes - 1) / L.passes : 0;
+    L.bits = L.passes ? std::max(4, (kb + L.passes - 1) / L.passes) : 0;
     const long long tiles = (n + RS_TILE - 1) / RS_TILE;
     const long long per = (tiles + RS_BLOCKS_MAX - 1) / RS_BLOCKS_MAX;
     L.chunk = std::max(1ll, per) * RS_TILE;
@@ -584,31 +670,45 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
     uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + L.keys[0]), reinterpret_cast<uint32_t*>(ws + L.keys[1])};
     uint32_t* vals[2] = {reinterpret_cast<uint32_t*>(ws + L.vals[0]), reinterpret_cast<uint32_t*>(ws + L.vals[1])};
     int* hist = reinterpret_cast<int*>(ws + L.hist);
+    const long long bytes = m * d * (long long)(dT_dt == DLRM_F32 ? 4 : 2);
+    // launches of the sort: a histogram takes about a third of a scatter's time, and so much of the zeros
+    const int shares = L.passes ? 4 * L.passes : 1;
+    long long done = 0;
+    auto zeros = [&](int sorters, int share) {
+        Zeros z{static_cast<char*>(dT), bytes * done / shares, bytes * (done + share) / shares, sorters};
+        done += share;
+        return z;
+    };
+    // blocks that write a share's zeros: 16 KB each at least, two per SM at most
+    auto writers = [&](const Zeros& z) {
+        return (unsigned)std::max<long long>(1, std::min<long long>((z.end - z.begin + 16383) / 16384, 2ll * device_sms()));
+    };
     int cur = 0;
     if (L.passes == 0) {
-        if (n > 0) {
-            int padded = 2;
-            while (padded < n) padded <<= 1;
-            const int threads = std::max(32, std::min(1024, padded / 2));
-            DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1), dim3(threads), sizeof(unsigned long long) * padded,
-                                      st, (int)n, padded, m, idx, keys[0], vals[0], err));
-        }
+        int padded = 2;
+        while (padded < n) padded <<= 1;
+        const int threads = std::max(256, std::min(1024, padded / 2));
+        const Zeros z = zeros(1, 1);
+        DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1 + writers(z)), dim3(threads),
+                                  sizeof(unsigned long long) * padded, st, (int)n, padded, m, idx, keys[0], vals[0], err, z));
     } else {
-        const dim3 grid(L.nblocks), block(RS_THREADS);
+        const dim3 block(RS_THREADS);
         for (int p = 0; p < L.passes; ++p) {
             const int shift = p * L.bits;
+            const Zeros zh = zeros(L.nblocks, 1), zs = zeros(L.nblocks, 3);
+            const dim3 gh(L.nblocks + writers(zh)), gs(L.nblocks + writers(zs));
             if (p == 0) {
-                DLRM_PDL_CHECK(launch_pdl(rs_hist_kernel<true>, grid, block, 0, st, n, m, (const void*)idx, shift,
-                                          L.bits, L.chunk, hist, err));
-                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<true>, grid, block, 0, st, n, m, (const void*)idx,
-                                          (const uint32_t*)nullptr, shift, L.bits, L.chunk, (const int*)hist, keys[0],
-                                          vals[0]));
+                DLRM_PDL_CHECK(launch_pdl(rs_hist_kernel<true>, gh, block, 0, st, n, m, (const void*)idx, shift,
+                                          L.bits, L.chunk, hist, err, zh));
+                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<true>, gs, block, 0, st, n, m, (const void*)idx,
+                                          (const uint32_t*)nullptr, shift, L.bits, L.chunk, (const int*)hist,
+                                          keys[0], vals[0], zs));
             } else {
-                DLRM_PDL_CHECK(launch_pdl(rs_hist_kernel<false>, grid, block, 0, st, n, m, (const void*)keys[cur], shift,
-                                          L.bits, L.chunk, hist, err));
-                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<false>, grid, block, 0, st, n, m, (const void*)keys[cur],
+                DLRM_PDL_CHECK(launch_pdl(rs_hist_kernel<false>, gh, block, 0, st, n, m, (const void*)keys[cur], shift,
+                                          L.bits, L.chunk, hist, err, zh));
+                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<false>, gs, block, 0, st, n, m, (const void*)keys[cur],
                                           (const uint32_t*)vals[cur], shift, L.bits, L.chunk, (const int*)hist,
-                                          keys[cur ^ 1], vals[cur ^ 1]));
+                                          keys[cur ^ 1], vals[cur ^ 1], zs));
                 cur ^= 1;
             }
         }
@@ -619,7 +719,7 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
     a.d = d;
     a.P = window_len(n, d);
     a.windows = (n + a.P - 1) / a.P;
-    a.wblocks = a.slices = 0;
+    a.slices = 0;
     a.keys = keys[cur];
     a.vals = vals[cur];
     a.dout = dout;

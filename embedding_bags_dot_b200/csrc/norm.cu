@@ -83,9 +83,21 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float (*red)[32], int sl
     return v;
 }
 
+// Rows ahead of the one being reduced are copied into shared memory asynchronously (cp.async): each thread copies
+// the 16-byte runs that it will itself read, so the ring needs no barrier.
+__device__ __forceinline__ void copy16_async(uint4* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+constexpr int FWD_RING = 3, BWD_RING = 2;    // rows in the ring: one in use, the others on their way
+
 // Thread t of the row's G threads holds runs t, t + G, ... (NV of them) of VEC elements.
-template <typename T, int VEC, int NV, bool BLOCK, bool Q8, int MAXT>
-__global__ void __launch_bounds__(MAXT) rmsnorm_fwd_kernel(const __grid_constant__ NormFwdArgs a) {
+template <typename T, int VEC, int NV, bool BLOCK, bool Q8, int MAXT, bool RING>
+__global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 1024 / MAXT) rmsnorm_fwd_kernel(const __grid_constant__ NormFwdArgs a) {
     pdl_wait();
     __shared__ float red[4][32];
     const int G = BLOCK ? blockDim.x : 32;
@@ -100,25 +112,53 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_fwd_kernel(const __grid_constant
             const int c = (t + i * G) * VEC + e;
             w[i][e] = a.w && c < a.d ? a.w[c] : 1.f;
         }
-    int slot = 0;
-    for (long long r = first; r < a.rows; r += step) {
-        const T* x = static_cast<const T*>(a.x) + r * a.ldx;
-        RowRaw<T, VEC> raw[NV], rres[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * G) * VEC;
-            if (c < a.d) raw[i].load(x + c);
-            else raw[i].zero();
-        }
-        if (a.res) {
+    int slot = 0, stage = 0;
+    RowRaw<T, VEC> raw[NV], rres[NV];
+    extern __shared__ uint4 ring[];      // RING: [row][x, residual][run][thread]
+    auto place = [&](int s, int arr, int i) { return ring + ((s * 2 + arr) * NV + i) * blockDim.x + threadIdx.x; };
+    auto send = [&](long long r, int s) {
+        if (r < a.rows) {
+            const T* x = static_cast<const T*>(a.x) + r * a.ldx;
             const T* res = static_cast<const T*>(a.res) + r * a.ldres;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (t + i * G) * VEC;
-                if (c < a.d) rres[i].load(res + c);
-                else rres[i].zero();
+                if (c < a.d) {
+                    copy16_async(place(s, 0, i), x + c);
+                    if (a.res) copy16_async(place(s, 1, i), res + c);
+                }
             }
         }
+        copy_commit();
+    };
+    if constexpr (RING) {
+#pragma unroll
+        for (int s = 0; s < FWD_RING - 1; ++s) send(first + s * step, s);
+    }
+    for (long long r = first; r < a.rows; r += step) {
+        if constexpr (RING) {
+            send(r + (FWD_RING - 1) * step, stage == 0 ? FWD_RING - 1 : stage - 1);
+            copy_wait<FWD_RING - 1>();
+        }
+        const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+        const T* res = static_cast<const T*>(a.res) + r * a.ldres;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * G) * VEC;
+            if (c < a.d) {
+                if constexpr (RING) {
+                    raw[i].a[0] = *place(stage, 0, i);
+                    if (a.res) rres[i].a[0] = *place(stage, 1, i);
+                } else {
+                    raw[i].load(x + c);
+                    if (a.res) rres[i].load(res + c);
+                }
+            } else {
+                raw[i].zero();
+                rres[i].zero();
+            }
+        }
+        if constexpr (RING) stage = stage + 1 == FWD_RING ? 0 : stage + 1;
         float v[NV][VEC], ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -164,17 +204,28 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_fwd_kernel(const __grid_constant
             const float amax = __uint_as_float(m), scale = amax / 448.f;
             if (t == 0) a.y_scale[r] = scale;
             uint8_t* y = static_cast<uint8_t*>(a.y) + r * a.ldy;
-            // 1 / scale would overflow or lose its subnormal bits for the smallest rows: those divide
-            const bool tiny = amax < 1e-30f;
-            const float inv = tiny ? 0.f : 448.f / amax;
+            if (amax >= 1e-30f || m > 0x7F800000u) {
+                const float inv = 448.f / amax;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (t + i * G) * VEC;
-                if (c < a.d) {
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (t + i * G) * VEC;
+                    if (c < a.d) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        v[i][e] = tiny ? (scale > 0.f ? v[i][e] / scale : 0.f) : v[i][e] * inv;
-                    store_e4m3<VEC>(y + c, v[i]);
+                        for (int e = 0; e < VEC; ++e) v[i][e] *= inv;
+                        store_e4m3<VEC>(y + c, v[i]);
+                    }
+                }
+            } else {
+                // 448 / amax could overflow here, and the scale may be a subnormal that says little about it
+                // (or zero): these rows divide by the scale as stored
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (t + i * G) * VEC;
+                    if (c < a.d) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) v[i][e] = scale > 0.f ? v[i][e] / scale : 0.f;
+                        store_e4m3<VEC>(y + c, v[i]);
+                    }
                 }
             }
         } else {
@@ -191,8 +242,8 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_fwd_kernel(const __grid_constant
     }
 }
 
-template <typename T, int VEC, int NV, bool BLOCK, int MAXT>
-__global__ void __launch_bounds__(MAXT) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+template <typename T, int VEC, int NV, bool BLOCK, int MAXT, bool RING>
+__global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : MAXT == 256 ? 3 : 4) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
     pdl_wait();
     __shared__ float red[2][32];
     const int G = BLOCK ? blockDim.x : 32;
@@ -208,31 +259,61 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_bwd_kernel(const __grid_constant
             w[i][e] = a.w && c < a.d ? a.w[c] : 1.f;
             dw[i][e] = 0.f;
         }
-    int slot = 0;
+    int slot = 0, stage = 0;
+    RowRaw<T, VEC> ry[NV], rh[NV], rd[NV];
+    extern __shared__ uint4 ring[];      // RING: [row][dy, h, dh][run][thread]
+    auto place = [&](int s, int arr, int i) { return ring + ((s * 3 + arr) * NV + i) * blockDim.x + threadIdx.x; };
+    auto send = [&](long long r, int s) {
+        if (r < a.rows) {
+            const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
+            const T* h = static_cast<const T*>(a.h) + r * a.ldh;
+            const T* dh = static_cast<const T*>(a.dh) + r * a.lddh;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (t + i * G) * VEC;
+                if (c < a.d) {
+                    copy16_async(place(s, 0, i), dy + c);
+                    copy16_async(place(s, 1, i), h + c);
+                    if (a.dh) copy16_async(place(s, 2, i), dh + c);
+                }
+            }
+        }
+        copy_commit();
+    };
+    if constexpr (RING) {
+#pragma unroll
+        for (int s = 0; s < BWD_RING - 1; ++s) send(first + s * step, s);
+    }
+    float next_rstd = first < a.rows ? a.rstd[first] : 0.f;
     for (long long r = first; r < a.rows; r += step) {
+        const float rstd = next_rstd;
+        if (r + step < a.rows) next_rstd = a.rstd[r + step];
+        if constexpr (RING) {
+            send(r + (BWD_RING - 1) * step, stage == 0 ? BWD_RING - 1 : stage - 1);
+            copy_wait<BWD_RING - 1>();
+        }
         const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
         const T* h = static_cast<const T*>(a.h) + r * a.ldh;
-        RowRaw<T, VEC> ry[NV], rh[NV], rd[NV];
+        const T* dh = static_cast<const T*>(a.dh) + r * a.lddh;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * G) * VEC;
             if (c < a.d) {
-                ry[i].load(dy + c);
-                rh[i].load(h + c);
+                if constexpr (RING) {
+                    ry[i].a[0] = *place(stage, 0, i);
+                    rh[i].a[0] = *place(stage, 1, i);
+                    if (a.dh) rd[i].a[0] = *place(stage, 2, i);
+                } else {
+                    ry[i].load(dy + c);
+                    rh[i].load(h + c);
+                    if (a.dh) rd[i].load(dh + c);
+                }
             } else {
                 ry[i].zero();
                 rh[i].zero();
             }
         }
-        if (a.dh) {
-            const T* dh = static_cast<const T*>(a.dh) + r * a.lddh;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (t + i * G) * VEC;
-                if (c < a.d) rd[i].load(dh + c);
-            }
-        }
-        const float rstd = a.rstd[r];
+        if constexpr (RING) stage = stage + 1 == BWD_RING ? 0 : stage + 1;
         float along = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -280,7 +361,7 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_bwd_kernel(const __grid_constant
             }
     } else {
         // the block's warps add their sums in warp order
-        extern __shared__ float sums[];   // [warps][NV * VEC * 32]
+        float* sums = reinterpret_cast<float*>(ring);   // [warps][NV * VEC * 32]
         constexpr int W = NV * VEC * 32;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -327,36 +408,41 @@ struct Runs {
     int vec() const { return bytes / es; }
 };
 
-template <typename T, int VEC, int NV, bool Q8>
-dlrm_status fwd_nv(const NormFwdArgs& a, cudaStream_t st) {
-    const int runs = (a.d + VEC - 1) / VEC;
-    if (runs <= 32 * NV) {
-        const int warps = 4;
-        const long long want = (a.rows + warps - 1) / warps, most = 16ll * device_sms();
-        DLRM_PDL_CHECK(launch_pdl(rmsnorm_fwd_kernel<T, VEC, NV, false, Q8, 128>,
-                                  dim3((unsigned)std::min(want, most)), dim3(32 * warps), 0, st, a));
-        return DLRM_OK;
-    }
-    const int threads = ((runs + NV - 1) / NV + 31) / 32 * 32;
-    const dim3 grid((unsigned)std::min<long long>(a.rows, (long long)device_sms() * std::max(1, 2048 / threads)));
-    if (threads <= 256)
-        DLRM_PDL_CHECK(launch_pdl(rmsnorm_fwd_kernel<T, VEC, NV, true, Q8, 256>, grid, dim3(threads), 0, st, a));
-    else if (threads <= 1024)
-        DLRM_PDL_CHECK(launch_pdl(rmsnorm_fwd_kernel<T, VEC, NV, true, Q8, 1024>, grid, dim3(threads), 0, st, a));
-    else
-        return DLRM_ERR_UNSUPPORTED;
+int norm_threads(int d, int per) { return ((d + per - 1) / per + 31) / 32 * 32; }
+
+// Launches a norm kernel with `smem` bytes of ring: at most 1,024 threads of 192 bytes. Above 48 KB in all the kernel has
+// to be told; always the same value, so that calls from several host threads agree.
+constexpr int RING_MOST = 1024 * 192;
+template <typename Args>
+dlrm_status norm_launch(void (*kern)(Args), unsigned grid, int threads, size_t smem, const Args& a, cudaStream_t st) {
+    if (smem > 40 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_MOST);
+    DLRM_PDL_CHECK(launch_pdl(kern, dim3(grid), dim3(threads), smem, st, a));
     return DLRM_OK;
 }
 
 template <typename T, int VEC, bool Q8>
 dlrm_status fwd_vec(const NormFwdArgs& a, cudaStream_t st) {
-    constexpr int W = 16 / (int)sizeof(T);       // elements of a full run
-    // few rows: the latency of one row counts, so it is spread over more threads
-    const bool few = a.rows <= device_sms();
-    const int runs = (a.d + VEC - 1) / VEC;
-    if (few && runs <= 1024) return fwd_nv<T, VEC, 1, Q8>(a, st);
-    if (runs <= 1024 * 2 * (W / VEC)) return fwd_nv<T, VEC, 2 * (W / VEC), Q8>(a, st);
-    return fwd_nv<T, VEC, 32 / VEC, Q8>(a, st);
+    constexpr int W = 16 / (int)sizeof(T);
+    constexpr int NV = W / VEC;             // one 16-byte run's elements, however they are loaded
+    const int one = norm_threads(a.d, W);
+    if (one == 32) {
+        const long long want = (a.rows + 3) / 4, most = 8ll * device_sms();
+        return norm_launch(rmsnorm_fwd_kernel<T, VEC, NV, false, Q8, 128, false>, (unsigned)std::min(want, most), 128, 0, a, st);
+    }
+    const long long sms = device_sms();
+    // few rows: the latency of a row counts, so it is spread over as many threads as it has runs
+    if (a.rows <= sms && one <= 1024)
+        return norm_launch(rmsnorm_fwd_kernel<T, VEC, NV, true, Q8, 1024, false>, (unsigned)a.rows, one, 0, a, st);
+    const int two = norm_threads(a.d, 2 * W);
+    if (two > 1024) {
+        const int t = norm_threads(a.d, 32);
+        return norm_launch(rmsnorm_fwd_kernel<T, VEC, 32 / VEC, true, Q8, 1024, false>,
+                           (unsigned)std::min<long long>(a.rows, sms), t, 0, a, st);
+    }
+    const unsigned grid = (unsigned)std::min<long long>(a.rows, sms * (1024 / two));
+    const size_t smem = VEC == W ? (size_t)FWD_RING * 2 * 2 * 16 * two : 0;
+    if (two > 256) return norm_launch(rmsnorm_fwd_kernel<T, VEC, 2 * NV, true, Q8, 1024, VEC == W>, grid, two, smem, a, st);
+    return norm_launch(rmsnorm_fwd_kernel<T, VEC, 2 * NV, true, Q8, 256, VEC == W>, grid, two, smem, a, st);
 }
 
 template <typename T>
@@ -374,39 +460,27 @@ dlrm_status fwd_t(const NormFwdArgs& a, bool q8, cudaStream_t st) {
     return q8 ? fwd_vec<T, 1, true>(a, st) : fwd_vec<T, 1, false>(a, st);
 }
 
-// Launch shape of the backward pass, shared with its workspace query: the number of blocks does not depend
-// on alignment, only on rows, so that the query needs no pointers.
-int bwd_blocks(int rows) { return std::max(1, std::min(rows, 4 * device_sms())); }
-
-template <typename T, int VEC, int NV>
-dlrm_status bwd_nv(const NormBwdArgs& a, int& nblocks, cudaStream_t st) {
-    const int runs = (a.d + VEC - 1) / VEC;
-    if (runs <= 32 * NV) {
-        const int warps = 4;
-        nblocks = bwd_blocks((a.rows + warps - 1) / warps);
-        const dim3 grid(nblocks);
-        const size_t smem = a.partial ? sizeof(float) * warps * NV * VEC * 32 : 0;
-        DLRM_PDL_CHECK(launch_pdl(rmsnorm_bwd_kernel<T, VEC, NV, false, 128>, grid, dim3(32 * warps), smem, st, a));
-        return DLRM_OK;
-    }
-    const int threads = ((runs + NV - 1) / NV + 31) / 32 * 32;
-    nblocks = bwd_blocks(a.rows);
-    const dim3 grid(nblocks);
-    if (threads <= 256)
-        DLRM_PDL_CHECK(launch_pdl(rmsnorm_bwd_kernel<T, VEC, NV, true, 256>, grid, dim3(threads), 0, st, a));
-    else if (threads <= 1024)
-        DLRM_PDL_CHECK(launch_pdl(rmsnorm_bwd_kernel<T, VEC, NV, true, 1024>, grid, dim3(threads), 0, st, a));
-    else
-        return DLRM_ERR_UNSUPPORTED;
-    return DLRM_OK;
-}
+// Most blocks of the backward pass, each of which writes a row of partial sums: about 1,024 threads per SM
+// at two 16-byte runs of a 16-bit type per thread.
+long long bwd_most(int d) { return (long long)device_sms() * std::max(1, std::min(8, 16384 / d)); }
 
 template <typename T, int VEC>
 dlrm_status bwd_vec(const NormBwdArgs& a, int& nblocks, cudaStream_t st) {
     constexpr int W = 16 / (int)sizeof(T);
-    const int runs = (a.d + VEC - 1) / VEC;
-    if (runs <= 1024 * 2 * (W / VEC)) return bwd_nv<T, VEC, 2 * (W / VEC)>(a, nblocks, st);
-    return bwd_nv<T, VEC, 32 / VEC>(a, nblocks, st);
+    constexpr int NV = W / VEC;
+    if (norm_threads(a.d, W) == 32) {
+        nblocks = (int)std::min<long long>((a.rows + 3) / 4, bwd_most(a.d));
+        const size_t smem = a.partial ? sizeof(float) * 4 * W * 32 : 0;
+        return norm_launch(rmsnorm_bwd_kernel<T, VEC, NV, false, 128, false>, nblocks, 128, smem, a, st);
+    }
+    const int two = norm_threads(a.d, 2 * W);
+    nblocks = (int)std::min<long long>(a.rows, bwd_most(a.d));
+    if (two > 1024)
+        return norm_launch(rmsnorm_bwd_kernel<T, VEC, 32 / VEC, true, 1024, false>, nblocks, norm_threads(a.d, 32), 0, a, st);
+    const size_t smem = VEC == W ? (size_t)BWD_RING * 3 * 2 * 16 * two : 0;
+    if (two > 256)
+        return norm_launch(rmsnorm_bwd_kernel<T, VEC, 2 * NV, true, 1024, VEC == W>, nblocks, two, smem, a, st);
+    return norm_launch(rmsnorm_bwd_kernel<T, VEC, 2 * NV, true, 256, VEC == W>, nblocks, two, smem, a, st);
 }
 
 template <typename T>
@@ -436,7 +510,7 @@ dlrm_status launch_rmsnorm_fwd(int rows, int d, const void* x, long long ldx, co
     return fwd_t<__nv_bfloat16>(a, q8, st);
 }
 
-size_t rmsnorm_bwd_partial_floats(int rows, int d) { return (size_t)bwd_blocks(rows) * d; }
+size_t rmsnorm_bwd_partial_floats(int rows, int d) { return (size_t)std::min<long long>(rows, bwd_most(d)) * d; }
 
 dlrm_status launch_rmsnorm_bwd(int rows, int d, const void* dy, long long lddy, const void* h, long long ldh,
                                const float* rstd, const float* w, const void* dh, long long lddh, dlrm_dtype dt,

@@ -16,6 +16,25 @@ template <> struct RawBytes<4> { using t = uint32_t; };
 template <> struct RawBytes<8> { using t = uint2; };
 template <> struct RawBytes<16> { using t = uint4; };
 
+// Two neighbouring elements at a time: one instruction widens or rounds both.
+template <typename T> struct Pair;
+template <> struct Pair<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 to_f(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t from_f(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+template <> struct Pair<__half> {
+    static __device__ __forceinline__ float2 to_f(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+    static __device__ __forceinline__ uint32_t from_f(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+
 // The stored form of a run: kept in this form while a load is in flight (half the registers of fp32).
 template <typename T, int VEC>
 struct RowRaw {
@@ -25,7 +44,9 @@ struct RowRaw {
     union {
         typename RawBytes<ACC>::t a[NA];
         T e[VEC];
+        uint32_t w[BYTES < 4 ? 1 : BYTES / 4];
     };
+    static constexpr bool PAIRS = sizeof(T) == 2 && VEC >= 2;
     __device__ __forceinline__ RowRaw() {}
     __device__ __forceinline__ void load(const T* p) {
         const typename RawBytes<ACC>::t* q = reinterpret_cast<const typename RawBytes<ACC>::t*>(p);
@@ -37,12 +58,26 @@ struct RowRaw {
         for (int i = 0; i < VEC; ++i) e[i] = Cvt<T>::from_f(0.f);
     }
     __device__ __forceinline__ void get(float (&v)[VEC]) const {
+        if constexpr (PAIRS) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = Cvt<T>::to_f(e[i]);
+            for (int i = 0; i < VEC; i += 2) {
+                const float2 f = Pair<T>::to_f(w[i / 2]);
+                v[i] = f.x;
+                v[i + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = Cvt<T>::to_f(e[i]);
+        }
     }
     __device__ __forceinline__ void set(const float (&v)[VEC]) {
+        if constexpr (PAIRS) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) e[i] = Cvt<T>::from_f(v[i]);
+            for (int i = 0; i < VEC; i += 2) w[i / 2] = Pair<T>::from_f(v[i], v[i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) e[i] = Cvt<T>::from_f(v[i]);
+        }
     }
     __device__ __forceinline__ void store(T* p) const {
         typename RawBytes<ACC>::t* q = reinterpret_cast<typename RawBytes<ACC>::t*>(p);
