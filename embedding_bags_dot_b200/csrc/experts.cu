@@ -23,8 +23,7 @@
 //  - expert_tile_kernel: tiles of 128 rows and 64 or 128 columns on one SM,
 //    forward only, for calls too small to fill the pairs, where reading the
 //    weights bounds the time. A row block of at most 32 rows loads 32 rows
-//    instead of 128. Calls of at most 32 rows (single tokens) take 32-column
-//    tiles with three quarters of the shared memory filled by weights on their way.
+//    instead of 128.
 // The tensor core truncates as it accumulates, so no accumulator runs longer
 // than 8 k-blocks (512 16-bit or 1,024 8-bit terms): the epilogue warps add each
 // finished part to fp32 registers, rounding to nearest, while the next part
@@ -44,9 +43,6 @@ namespace tc {
 
 constexpr int EX_MAX = DLRM_MAX_EXPERTS;
 constexpr int PART = 8;                             // k-blocks per accumulator
-#ifndef EX_FEWW
-#define EX_FEWW 32
-#endif
 constexpr int EX_THREADS2 = 384;                    // pair kernel: warps 0..3 TMA, MMA, idle; 4..11 epilogue
 constexpr int EX_REGS_LOW = 40, EX_REGS_HIGH = 232;
 static_assert(128 * EX_REGS_LOW + 256 * EX_REGS_HIGH <= 168 * EX_THREADS2, "register split exceeds the launch allocation");
@@ -247,15 +243,15 @@ template <int NC>
 __device__ __forceinline__ void ex_promote(float (&acc)[NC][32], uint32_t taddr) {
 #pragma unroll
     for (int c = 0; c < NC; c += 2) {
-        constexpr int W = NC < 2 ? NC : 2;
-        float r[W][32];
-#pragma unroll
-        for (int i = 0; i < W; ++i) tmem_ld32_f(taddr + 32 * (c + i), r[i]);
+        float r[2][32];
+        tmem_ld32_f(taddr + 32 * c, r[0]);
+        tmem_ld32_f(taddr + 32 * c + 32, r[1]);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) acc[c + i][e] += r[i][e];
+        for (int e = 0; e < 32; ++e) {
+            acc[c][e] += r[0][e];
+            acc[c + 1][e] += r[1][e];
+        }
     }
 }
 
@@ -372,33 +368,6 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>&
                 }
             }
             __syncwarp();
-        }
-    }
-}
-
-// At most 32 rows x 32 columns, straight from registers: each lane writes its row's 64 or 128 bytes.
-template <typename TC, int KIND>
-__device__ __forceinline__ void ex_store_few(float (&v)[32], const EpiRow<1>& er, int row0, int nvalid, int j0,
-                                             const ExpertArgs& a) {
-    const int lane = threadIdx.x & 31;
-    ex_affine<1, KIND>(v, er, 0, a);
-    if (lane >= nvalid) return;
-    TC* dst = static_cast<TC*>(a.C) + (long long)(row0 + lane) * a.ldc + j0;
-    constexpr int E16 = 16 / (int)sizeof(TC);
-#pragma unroll
-    for (int q = 0; q < 32 / E16; ++q) {
-        union {
-            TC t[E16];
-            uint4 w;
-        } u;
-#pragma unroll
-        for (int k = 0; k < E16; ++k) u.t[k] = Cvt<TC>::from_f(v[q * E16 + k]);
-        if (j0 + (q + 1) * E16 <= a.J) {
-            *reinterpret_cast<uint4*>(dst + q * E16) = u.w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < E16; ++k)
-                if (j0 + q * E16 + k < a.J) dst[q * E16 + k] = u.t[k];
         }
     }
 }
@@ -614,28 +583,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
 
 // ------------------------------------------------------------------ one SM per tile (forward)
 
-// BNT: tile columns (weight rows); AR: rows of X a stage holds.
-template <int BNT_, int AR_, int NS_, int WC_>
-struct ExTileT {
-    static constexpr int BNT = BNT_, AR = AR_, NS = NS_;
-    static constexpr int WC = WC_;                             // columns per epilogue warp
-    static constexpr int STAGE = (AR + BNT) * 128;
+template <int BNT>
+struct ExTile {
+    static constexpr int NS = BNT == 64 ? 8 : 6;
+    static constexpr int STAGE = (128 + BNT) * 128;
     static constexpr int TMEM = 2 * BNT;
+    static constexpr int WC = 64;                            // columns per epilogue warp
     static constexpr int SMEM = NS * STAGE + OUT_BYTES + (int)sizeof(Ranges) + (int)sizeof(ExBars<NS>) + 256;
 };
-template <int BNT>
-using ExTile = ExTileT<BNT, 128, BNT == 64 ? 8 : 6, BNT == 64 ? 64 : BNT / 2>;
-// Calls of at most 32 rows: a stage holds 32 rows of X and 32 of W, 24 stages deep, so that each SM has about 96 KB
-// of weights on their way. The MMA still reads 128 rows from a stage's first byte on: rows past the 32 are
-// whatever the next blocks of shared memory hold (the last stage's end in the output buffers) and only reach
-// accumulator rows that are never read.
-using ExFew = ExTileT<32, 32, 24, 32>;
-static_assert((ExFew::NS - 1) * ExFew::STAGE + 128 * 128 <= ExFew::NS * ExFew::STAGE + OUT_BYTES, "128 rows stay inside");
 
-template <typename TC, int KIND, typename T>
+template <typename TC, int KIND, int BNT>
 __global__ void __launch_bounds__(THREADS, 1)
     expert_tile_kernel(const __grid_constant__ ExpertMaps maps, const __grid_constant__ ExpertArgs a, uint32_t id) {
-    constexpr int NS = T::NS, BNT = T::BNT, AR = T::AR;
+    using T = ExTile<BNT>;
+    constexpr int NS = T::NS;
     constexpr int KE = KIND == EX_F8 ? 128 : 64;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = su32(smem_raw);
@@ -683,7 +644,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ph = 0;
         for (long long t = blockIdx.x; !timed_out && uni(walk.seek(t, mb, cb)); t += gridDim.x) {
             const int e = uni(walk.e), row = uni(rg->begin[e] + mb * 128), col = uni(cb) * BNT;
-            const bool few = AR == 32 || uni(rg->end[e]) - row <= 32;
+            const bool few = uni(rg->end[e]) - row <= 32;
             const uint32_t tx = (uint32_t)((few ? 32 : 128) + BNT) * 128u;
             for (int kb = 0; kb < nk; ++kb) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&bars->empty[s], ph ^ 1u, abort))) {
@@ -695,7 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mbar_expect_tx(&bars->full[s], tx);
                     if (few) tma_load_2d(sa, &maps.a32, &bars->full[s], kb * KE, row);
                     else tma_load_2d(sa, &maps.a, &bars->full[s], kb * KE, row);
-                    ex_load_3d(sa + AR * 128, &maps.b, &bars->full[s], kb * KE, col, e);
+                    ex_load_3d(sa + 128 * 128, &maps.b, &bars->full[s], kb * KE, col, e);
                 }
                 __syncwarp();
                 if (++s == NS) {
@@ -715,7 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_wait(&bars->full[s], ph, abort, true);
         }
     } else if (warp == 1) {
-        const uint64_t a0 = sdesc(base), b0 = sdesc(base + AR * 128);
+        const uint64_t a0 = sdesc(base), b0 = sdesc(base + 128 * 128);
         const uint32_t ahi = (uint32_t)(a0 >> 32), bhi = (uint32_t)(b0 >> 32);
         int s = 0;
         uint32_t ph = 0, part = 0;
@@ -785,10 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(&bars->tempty[b]);
             }
             if (timed_out) break;
-            if (some) {
-                if constexpr (AR == 32) ex_store_few<TC, KIND>(acc[0], er, row, nvalid, j0, a);
-                else ex_store<TC, NC, EX_FWD, KIND, 1>(acc, er, row, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
-            }
+            if (some) ex_store<TC, NC, EX_FWD, KIND, 1>(acc, er, row, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
         }
         if (timed_out) *abort = 1;
         if (lane == 0) bulk_wait_all0();
@@ -806,7 +764,7 @@ template <int KIND>
 constexpr int EX_SMEM2 = ExPair<KIND>::NS * EX_STAGE2_BYTES + ExPair<KIND>::OUT + (int)sizeof(Ranges) +
                          (int)sizeof(ExBars<ExPair<KIND>::NS>) + 256;
 static_assert(EX_SMEM2<EX_F16> <= 227 * 1024 && EX_SMEM2<EX_F8> <= 227 * 1024, "shared memory");
-static_assert(ExTile<64>::SMEM <= 227 * 1024 && ExTile<128>::SMEM <= 227 * 1024 && ExFew::SMEM <= 227 * 1024, "shared memory");
+static_assert(ExTile<64>::SMEM <= 227 * 1024 && ExTile<128>::SMEM <= 227 * 1024, "shared memory");
 
 // ------------------------------------------------------------------ backward: dP, bias sums, padded last blocks
 
@@ -1031,14 +989,15 @@ dlrm_status launch_pair(const ExpertMaps& maps, const ExpertArgs& a, uint32_t id
     return DLRM_OK;
 }
 
-template <typename TC, int KIND, typename T>
+template <typename TC, int KIND, int BNT>
 dlrm_status launch_tile(const ExpertMaps& maps, const ExpertArgs& a, int fmt, cudaStream_t st) {
-    auto kern = expert_tile_kernel<TC, KIND, T>;
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
-    const long long tiles = most_tiles(a.E, a.M, 128, (a.J + T::BNT - 1) / T::BNT);
+    auto kern = expert_tile_kernel<TC, KIND, BNT>;
+    constexpr int SMEM = ExTile<BNT>::SMEM;
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    const long long tiles = most_tiles(a.E, a.M, 128, (a.J + BNT - 1) / BNT);
     const dim3 grid((unsigned)std::min<long long>(tiles, device_sms()));
-    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(THREADS), (size_t)T::SMEM, st, maps, a,
-                              ex_idesc(fmt, false, false, 128, T::BNT)));
+    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(THREADS), (size_t)SMEM, st, maps, a,
+                              ex_idesc(fmt, false, false, 128, BNT)));
     return DLRM_OK;
 }
 
@@ -1052,25 +1011,27 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
     using namespace tc;
     const int es = ex_size(dt), ke = 128 / es;
     ExpertArgs a{E, M, N, 0, K, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, err};
-    // SM pairs once their 256 x 256 tiles can fill them (rows spread evenly over the experts); otherwise one SM
-    // per tile, of the width whose last round over the SMs wastes least
+    // SM pairs once their 256 x 256 tiles can fill them (rows spread evenly over the experts). Otherwise one SM per
+    // tile: 64 columns wide if that gives every tile an SM of its own, else 128 (12 rows of 8 experts, 4,096 x 1,024
+    // bf16: 13.6 us at 128, 15.5 at 64, 17.6 at 32; a k-block's issue costs 420 to 465 cycles at any width).
     const long long nb2 = (N + 255) / 256, sms = device_sms();
-    const bool few = M <= 32 && EX_FEWW == 32, pair = !few && ((long long)M / 256) * nb2 >= sms / 2;
+    const bool pair = ((long long)M / 256) * nb2 >= sms / 2;
     const long long rb = std::max<long long>((M + 127) / 128, std::min(E, M));
-    auto rounds = [&](int w) { return (rb * ((N + w - 1) / w) + sms - 1) / sms * w; };
-    const int bnt = few ? 32 : M <= 32 ? EX_FEWW : rounds(128) <= rounds(64) ? 128 : 64;
+    const bool narrow = rb * ((N + 63) / 64) <= sms;
     ExpertMaps maps{};
-    if (!ex_map(&maps.a, X, es, dt, 2, K, M, 1, ldx, ke, 128) || !ex_map(&maps.a32, X, es, dt, 2, K, M, 1, ldx, ke, 32) ||
-        !ex_map(&maps.b, W, es, dt, 3, K, N, E, ldw, ke, pair ? 128 : bnt) ||
+    // the tile kernel's A comes in boxes of 128 rows or, for row blocks of at most 32, of 32
+    const bool only32 = !pair && M <= 32;
+    if ((!only32 && !ex_map(&maps.a, X, es, dt, 2, K, M, 1, ldx, ke, 128)) ||
+        (!pair && !ex_map(&maps.a32, X, es, dt, 2, K, M, 1, ldx, ke, 32)) ||
+        !ex_map(&maps.b, W, es, dt, 3, K, N, E, ldw, ke, pair || !narrow ? 128 : 64) ||
         !ex_map(&maps.c, Y, ex_size(y_dt), y_dt, 2, N, M, 1, ldy, 128 / ex_size(y_dt), 32))
         return DLRM_ERR_CUDA;
     const int fmt = dt == DLRM_BF16 ? 1 : 0;
-#define DLRM_EX_FWD(TC, KIND)                                                                                    \
-    return pair ? launch_pair<TC, EX_FWD, KIND>(maps, a, ex_idesc(fmt, false, false, 256, 256),                  \
-                                                most_tiles(E, M, 256, nb2), st)                                  \
-           : few        ? launch_tile<TC, KIND, ExFew>(maps, a, fmt, st)                                         \
-           : bnt == 128 ? launch_tile<TC, KIND, ExTile<128>>(maps, a, fmt, st)                                   \
-                        : launch_tile<TC, KIND, ExTile<64>>(maps, a, fmt, st);
+#define DLRM_EX_FWD(TC, KIND)                                                                     \
+    return pair ? launch_pair<TC, EX_FWD, KIND>(maps, a, ex_idesc(fmt, false, false, 256, 256),   \
+                                                most_tiles(E, M, 256, nb2), st)                   \
+           : narrow ? launch_tile<TC, KIND, 64>(maps, a, fmt, st)                                 \
+                    : launch_tile<TC, KIND, 128>(maps, a, fmt, st);
     if (dt == DLRM_E4M3) {
         if (y_dt == DLRM_F32) DLRM_EX_FWD(float, EX_F8)
         if (y_dt == DLRM_BF16) DLRM_EX_FWD(__nv_bfloat16, EX_F8)

@@ -8,9 +8,10 @@
 //
 // Backward: n rows of dout read once, m rows of the table's gradient written
 // once; no atomics on values, so the result does not depend on timing.
-//   1. (id, position) pairs are sorted by id, stably: one block's bitonic
-//      sort in shared memory for short calls, else an LSD radix sort whose
-//      digits are as wide as the table needs (two passes up to 2^20 rows).
+//   1. (id, position) pairs are sorted by id, stably: an LSD radix sort whose
+//      digits are as wide as the table needs (two passes up to 2^20 rows), in
+//      one block's shared memory up to 4,096 pairs, else a histogram and a
+//      scatter per pass over blocks of 2,048.
 //      The sort takes few SMs and little bandwidth, so the other blocks of
 //      its launches write the table's zeros meanwhile; rows with lookups are
 //      written again by the next steps.
@@ -129,12 +130,15 @@ dlrm_status lookup_ti(const LookupArgs& a, dlrm_dtype out_dt, cudaStream_t st) {
 
 // ------------------------------------------------------------------ sort of (id, position)
 
-constexpr int SORT1_MAX = 4096;        // pairs the one-block sort takes
-constexpr int DIG_BITS_MAX = 10;
-constexpr int RS_THREADS = 256;
+constexpr int DIG_BITS_MAX = 10;       // digits of up to 10 bits
 constexpr int RS_ITEMS = 8;            // keys per thread and tile
+// Ranking a warp's 32 keys costs about a hundred instructions, so a pass takes an SM the longer the more of them it
+// has: 8,192 pairs on one SM took 10 us a pass. Blocks are small, and short calls alone stay in one.
+constexpr int RS_THREADS = 256;
 constexpr int RS_TILE = RS_THREADS * RS_ITEMS;
 constexpr int RS_BLOCKS_MAX = 296;
+constexpr int SORT1_THREADS = 512;     // the one-block sort takes up to 4,096 pairs
+constexpr int SORT1_MAX = SORT1_THREADS * RS_ITEMS;
 
 // A share of the table's bytes, zeroed by the blocks of a sorting launch that do not sort.
 struct Zeros {
@@ -159,51 +163,6 @@ __device__ __forceinline__ void write_zeros(const Zeros& z) {
     }
 }
 
-// The whole sort in one block: bitonic over 64-bit words (id, position), which are all different, so the
-// order is that of a stable sort by id. Indices outside the table get id m and end up last.
-__global__ void __launch_bounds__(1024) sort_one_block_kernel(int n, int padded, long long m,
-                                                              const int32_t* __restrict__ idx,
-                                                              uint32_t* __restrict__ keys,
-                                                              uint32_t* __restrict__ vals, ErrRecord* err,
-                                                              const __grid_constant__ Zeros zeros) {
-    pdl_wait();
-    extern __shared__ unsigned long long pairs[];
-    if (blockIdx.x > 0) {
-        write_zeros(zeros);
-        return;
-    }
-    unsigned bad = 0;
-    for (int i = threadIdx.x; i < padded; i += blockDim.x) {
-        unsigned long long p = ~0ull;
-        if (i < n) {
-            const int v = idx[i];
-            const bool ok = v >= 0 && v < m;
-            bad += !ok;
-            p = ((unsigned long long)(ok ? (uint32_t)v : (uint32_t)m) << 32) | (uint32_t)i;
-        }
-        pairs[i] = p;
-    }
-    report_warp(err, bad, 0);
-    for (int size = 2; size <= padded; size <<= 1) {
-        for (int step = size >> 1; step; step >>= 1) {
-            __syncthreads();
-            for (int t = threadIdx.x; t < padded / 2; t += blockDim.x) {
-                const int lo = ((t & ~(step - 1)) << 1) | (t & (step - 1)), hi = lo | step;
-                const unsigned long long x = pairs[lo], y = pairs[hi];
-                if ((x > y) == ((lo & size) == 0)) {
-                    pairs[lo] = y;
-                    pairs[hi] = x;
-                }
-            }
-        }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        keys[i] = (uint32_t)(pairs[i] >> 32);
-        vals[i] = (uint32_t)pairs[i];
-    }
-}
-
 // Radix pass: block b owns keys [b * chunk, (b + 1) * chunk). FIRST reads the indices themselves.
 template <bool FIRST>
 __device__ __forceinline__ uint32_t pass_key(const void* in, long long i, long long m) {
@@ -212,6 +171,155 @@ __device__ __forceinline__ uint32_t pass_key(const void* in, long long i, long l
         return v >= 0 && v < m ? (uint32_t)v : (uint32_t)m;
     } else {
         return static_cast<const uint32_t*>(in)[i];
+    }
+}
+
+// Shared memory of a sorting block of W warps.
+struct SortMem {
+    unsigned short* wc;     // [W][radix]: keys of a digit in each warp, then their places by warp
+    int* tot;               // [radix]
+    int* wsum;              // [32]
+    uint32_t* keys;         // [tile]: the tile's pairs in order
+    uint32_t* vals;
+};
+__device__ __forceinline__ SortMem sort_mem(unsigned char* p, int warps, int radix) {
+    SortMem s;
+    s.wc = reinterpret_cast<unsigned short*>(p);
+    s.tot = reinterpret_cast<int*>(p + 2 * warps * radix);
+    s.wsum = s.tot + radix;
+    s.keys = reinterpret_cast<uint32_t*>(s.wsum + 32);
+    s.vals = s.keys + warps * 32 * RS_ITEMS;
+    return s;
+}
+size_t sort_bytes(int warps, int radix) {
+    return 2 * (size_t)warps * radix + 4 * (size_t)radix + 128 + 8 * (size_t)warps * 32 * RS_ITEMS;
+}
+
+// place[e] = how many keys of the block with the same digit come before the thread's e-th; sm.tot[digit] = how many
+// there are. Key e of lane l in warp w is number w * 256 + e * 32 + l of the tile; those from `cnt` on do not count.
+// Each warp counts its own keys 32 at a time (equal digits find each other by match), then each digit's counts
+// are summed over the warps.
+__device__ __forceinline__ void rank_keys(const uint32_t (&key)[RS_ITEMS], int cnt, int shift, int radix, const SortMem& sm,
+                                          int (&place)[RS_ITEMS]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int first = warp * (32 * RS_ITEMS) + lane;
+    for (int i = threadIdx.x; i < warps * radix / 8; i += blockDim.x)
+        reinterpret_cast<uint4*>(sm.wc)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    unsigned short* mine = sm.wc + warp * radix;
+    const unsigned lt = (1u << lane) - 1u;
+#pragma unroll
+    for (int e = 0; e < RS_ITEMS; ++e) {
+        const bool valid = first + e * 32 < cnt;
+        const int dg = valid ? (int)((key[e] >> shift) & (radix - 1)) : radix;   // radix: no digit
+        const unsigned peers = __match_any_sync(0xffffffffu, dg);
+        const int ahead = __popc(peers & lt);
+        const int seen = valid ? mine[dg] : 0;
+        place[e] = seen + ahead;
+        __syncwarp();
+        if (valid && ahead == 0) mine[dg] = (unsigned short)(seen + __popc(peers));
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int dg = threadIdx.x; dg < radix; dg += blockDim.x) {
+        int run = 0;
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) {
+            const int c = sm.wc[w * radix + dg];
+            sm.wc[w * radix + dg] = (unsigned short)run;
+            run += c;
+        }
+        sm.tot[dg] = run;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < RS_ITEMS; ++e)
+        if (first + e * 32 < cnt) place[e] += mine[(key[e] >> shift) & (radix - 1)];
+}
+
+// x[0..radix) becomes its exclusive prefix sums, by the whole block (radix <= 4 blockDim).
+__device__ __forceinline__ void scan_digits(int* x, int radix, int* wsum) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (radix + blockDim.x - 1) / blockDim.x;
+    int v[4], s = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = threadIdx.x * per + e;
+        v[e] = e < per && i < radix ? x[i] : 0;
+        s += v[e];
+    }
+    int incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int run = incl - s;
+    for (int q = 0; q < warp; ++q) run += wsum[q];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = threadIdx.x * per + e;
+        if (e < per && i < radix) x[i] = run;
+        run += v[e];
+    }
+    __syncthreads();
+}
+
+// The whole sort in one block, the pairs going round through shared memory. Indices outside the table get id m
+// and end up last.
+__global__ void __launch_bounds__(SORT1_THREADS) sort_one_block_kernel(int n, long long m, int passes, int bits,
+                                                                    const int32_t* __restrict__ idx,
+                                                                    uint32_t* __restrict__ keys,
+                                                                    uint32_t* __restrict__ vals, ErrRecord* err,
+                                                                    const __grid_constant__ Zeros zeros) {
+    pdl_wait();
+    extern __shared__ __align__(16) unsigned char sort_smem[];
+    if (blockIdx.x > 0) {
+        write_zeros(zeros);
+        return;
+    }
+    const int radix = 1 << bits;
+    const SortMem sm = sort_mem(sort_smem, blockDim.x >> 5, radix);
+    const int first = (threadIdx.x >> 5) * (32 * RS_ITEMS) + (threadIdx.x & 31);
+    uint32_t key[RS_ITEMS], val[RS_ITEMS];
+    unsigned bad = 0;
+#pragma unroll
+    for (int e = 0; e < RS_ITEMS; ++e) {
+        const int i = first + e * 32;
+        key[e] = val[e] = 0;
+        if (i < n) {
+            key[e] = pass_key<true>(idx, i, m);
+            val[e] = (uint32_t)i;
+            bad += key[e] == (uint32_t)m;
+        }
+    }
+    report_warp(err, bad, 0);
+    for (int p = 0; p < passes; ++p) {
+        int place[RS_ITEMS];
+        rank_keys(key, n, p * bits, radix, sm, place);
+        scan_digits(sm.tot, radix, sm.wsum);
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e)
+            if (first + e * 32 < n) {
+                const int at = sm.tot[(key[e] >> (p * bits)) & (radix - 1)] + place[e];
+                sm.keys[at] = key[e];
+                sm.vals[at] = val[e];
+            }
+        __syncthreads();
+        if (p + 1 < passes) {
+#pragma unroll
+            for (int e = 0; e < RS_ITEMS; ++e)
+                if (first + e * 32 < n) {
+                    key[e] = sm.keys[first + e * 32];
+                    val[e] = sm.vals[first + e * 32];
+                }
+        }
+    }
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        keys[i] = sm.keys[i];
+        vals[i] = sm.vals[i];
     }
 }
 
@@ -232,10 +340,17 @@ __global__ void __launch_bounds__(RS_THREADS) rs_hist_kernel(long long n, long l
     __syncthreads();
     const long long b0 = (long long)blockIdx.x * chunk, b1 = b0 + chunk < n ? b0 + chunk : n;
     unsigned bad = 0;
-    for (long long i = b0 + threadIdx.x; i < b1; i += blockDim.x) {
-        const uint32_t k = pass_key<FIRST>(in, i, m);
-        if (FIRST) bad += k == (uint32_t)m;
-        atomicAdd(&h[(k >> shift) & (radix - 1)], 1);
+    for (long long i0 = b0 + threadIdx.x; i0 < b1; i0 += RS_TILE) {
+        uint32_t key[RS_ITEMS];
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e)
+            if (i0 + e * RS_THREADS < b1) key[e] = pass_key<FIRST>(in, i0 + e * RS_THREADS, m);
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e)
+            if (i0 + e * RS_THREADS < b1) {
+                if (FIRST) bad += key[e] == (uint32_t)m;
+                atomicAdd(&h[(key[e] >> shift) & (radix - 1)], 1);
+            }
     }
     if (FIRST) {
         __syncwarp();
@@ -255,44 +370,39 @@ __global__ void __launch_bounds__(RS_THREADS) rs_scatter_kernel(long long n, lon
                                                                 uint32_t* __restrict__ vout,
                                                                 const __grid_constant__ Zeros zeros) {
     pdl_wait();
+    extern __shared__ __align__(16) unsigned char sort_smem[];
+    __shared__ int next[1 << DIG_BITS_MAX];      // the block's next output position per digit
     if ((int)blockIdx.x >= zeros.sorters) {
         write_zeros(zeros);
         return;
     }
-    constexpr int W = RS_THREADS / 32;
-    constexpr int RMAX = 1 << DIG_BITS_MAX;
-    constexpr int PER = RMAX / RS_THREADS;     // digits per thread: consecutive
-    __shared__ int next[RMAX];                 // the block's next output position per digit
-    __shared__ __align__(16) unsigned short wcount[W][RMAX]; // keys of a digit met so far by each warp in this tile
-    __shared__ int wsum[W];
     const int radix = 1 << bits;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const SortMem sm = sort_mem(sort_smem, RS_THREADS / 32, radix);
     const long long b0 = (long long)blockIdx.x * chunk, b1 = b0 + chunk < n ? b0 + chunk : n;
-    // warp w takes a tile's keys [w, w + 1) * 32 * RS_ITEMS, 32 at a time in order; the first tile's are on their
-    // way while the positions are worked out
+    const int first = (threadIdx.x >> 5) * (32 * RS_ITEMS) + (threadIdx.x & 31);
     uint32_t key[RS_ITEMS], val[RS_ITEMS];
     auto load_tile = [&](long long t0) {
 #pragma unroll
         for (int e = 0; e < RS_ITEMS; ++e) {
-            const long long i = t0 + warp * (32 * RS_ITEMS) + e * 32 + lane;
+            const long long i = t0 + first + e * 32;
             const bool valid = i < b1;
             key[e] = valid ? pass_key<FIRST>(in, i, m) : 0u;
             val[e] = valid ? (FIRST ? (uint32_t)i : vin[i]) : 0u;
         }
     };
-    load_tile(b0);
-    // totals and prefixes over blocks: each thread takes four neighbouring digits, and the threads left over share
-    // the blocks' rows between them
-    int* tot = reinterpret_cast<int*>(wcount);           // [groups][radix]: 1,024 sums in all
-    int* bef = tot + 4 * RS_THREADS;
-    const int per_group = radix / 4, groups = RS_THREADS / per_group;
+    load_tile(b0);      // on its way while the positions are worked out
     {
+        // totals and prefixes over blocks: each thread takes four neighbouring digits, and the threads left over
+        // share the blocks' rows between them
+        int* tot = reinterpret_cast<int*>(sm.keys);          // [groups][radix]: 4 * RS_THREADS sums
+        int* bef = tot + 4 * RS_THREADS;
+        const int per_group = radix / 4, groups = RS_THREADS / per_group;
         const int g = threadIdx.x / per_group, d4 = threadIdx.x - g * per_group;
         const int nb = zeros.sorters, mine = (nb + groups - 1) / groups;
         const int q0 = g * mine, q1 = q0 + mine < nb ? q0 + mine : nb;
         int4 all = make_int4(0, 0, 0, 0), before = all;
         const int4* row = reinterpret_cast<const int4*>(hist) + d4;
-#pragma unroll 16
+#pragma unroll 8
         for (int q = q0; q < q1; ++q) {
             const int4 v = __ldg(row + (long long)q * per_group);
             all.x += v.x, all.y += v.y, all.z += v.z, all.w += v.w;
@@ -300,91 +410,46 @@ __global__ void __launch_bounds__(RS_THREADS) rs_scatter_kernel(long long n, lon
         }
         reinterpret_cast<int4*>(tot)[threadIdx.x] = all;
         reinterpret_cast<int4*>(bef)[threadIdx.x] = before;
-    }
-    __syncthreads();
-    for (int dg = threadIdx.x; dg < radix; dg += RS_THREADS) {
-        int all = 0, before = 0;
-        for (int g = 0; g < groups; ++g) {
-            all += tot[g * radix + dg];
-            before += bef[g * radix + dg];
-        }
-        next[dg] = all;
-        bef[dg] = before;      // only this thread reads or writes column dg
-    }
-    for (int dg = radix + threadIdx.x; dg < RMAX; dg += RS_THREADS) next[dg] = 0;
-    __syncthreads();
-    {
-        int v[PER], s = 0;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            v[e] = next[threadIdx.x * PER + e];
-            s += v[e];
-        }
-        int incl = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
-        }
-        if (lane == 31) wsum[warp] = incl;
         __syncthreads();
-        int base = incl - s;
-        for (int q = 0; q < warp; ++q) base += wsum[q];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            const int dg = threadIdx.x * PER + e;
-            if (dg < radix) next[dg] = base + bef[dg];
-            base += v[e];
-        }
-    }
-    __syncthreads();
-    const unsigned lt = (1u << lane) - 1u;
-    for (long long t0 = b0; t0 < b1; t0 += RS_TILE) {
-        for (int i = threadIdx.x; i < W * per_group * 2; i += RS_THREADS)
-            reinterpret_cast<uint32_t*>(wcount[i / (per_group * 2)])[i % (per_group * 2)] = 0;
-        __syncthreads();
-        if (t0 > b0) load_tile(t0);
-        const long long w0 = t0 + (long long)warp * (32 * RS_ITEMS);
-        int rank[RS_ITEMS];
-#pragma unroll
-        for (int e = 0; e < RS_ITEMS; ++e) {
-            const bool valid = w0 + e * 32 + lane < b1;
-            const int dg = valid ? (int)((key[e] >> shift) & (radix - 1)) : radix;   // radix: no digit
-            const unsigned peers = __match_any_sync(0xffffffffu, dg);
-            const int ahead = __popc(peers & lt);
-            const int cnt = valid ? wcount[warp][dg] : 0;
-            rank[e] = valid ? cnt + ahead : -1;
-            __syncwarp();
-            if (valid && ahead == 0) wcount[warp][dg] = (unsigned short)(cnt + __popc(peers));
-            __syncwarp();
-        }
-        __syncthreads();
-        // counts -> positions within the block's run of that digit, by warp; next moves on by the tile's total
         for (int dg = threadIdx.x; dg < radix; dg += RS_THREADS) {
-            int run = 0;
-#pragma unroll
-            for (int q = 0; q < W; ++q) {
-                const int c = wcount[q][dg];
-                wcount[q][dg] = (unsigned short)run;
-                run += c;
+            int x = 0, y = 0;
+            for (int q = 0; q < groups; ++q) {
+                x += tot[q * radix + dg];
+                y += bef[q * radix + dg];
             }
+            next[dg] = x;
+            bef[dg] = y;        // only this thread reads or writes column dg
         }
         __syncthreads();
-#pragma unroll
-        for (int e = 0; e < RS_ITEMS; ++e) {
-            if (rank[e] >= 0) {
-                const int dg = (int)((key[e] >> shift) & (radix - 1));
-                const long long pos = (long long)next[dg] + wcount[warp][dg] + rank[e];
-                kout[pos] = key[e];
-                vout[pos] = val[e];
-                rank[e] += wcount[warp][dg];
-            }
-        }
+        scan_digits(next, radix, sm.wsum);
+        for (int dg = threadIdx.x; dg < radix; dg += RS_THREADS) next[dg] += bef[dg];
         __syncthreads();
-        // next position after the tile: one past the largest rank of each digit
+    }
+    for (long long t0 = b0; t0 < b1; t0 += RS_TILE) {
+        if (t0 > b0) load_tile(t0);
+        const int cnt = (int)(b1 - t0 < RS_TILE ? b1 - t0 : RS_TILE);
+        int place[RS_ITEMS];
+        rank_keys(key, cnt, shift, radix, sm, place);
+        scan_digits(sm.tot, radix, sm.wsum);
+        // in order of digit through shared memory, so that neighbouring threads write neighbouring pairs
 #pragma unroll
         for (int e = 0; e < RS_ITEMS; ++e)
-            if (rank[e] >= 0) atomicAdd(&next[(key[e] >> shift) & (radix - 1)], 1);
+            if (first + e * 32 < cnt) {
+                const int at = sm.tot[(key[e] >> shift) & (radix - 1)] + place[e];
+                sm.keys[at] = key[e];
+                sm.vals[at] = val[e];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < cnt; i += RS_THREADS) {
+            const uint32_t k = sm.keys[i];
+            const int dg = (int)((k >> shift) & (radix - 1));
+            const long long at = (long long)next[dg] + (i - sm.tot[dg]);
+            kout[at] = k;
+            vout[at] = sm.vals[i];
+        }
+        __syncthreads();
+        for (int dg = threadIdx.x; dg < radix; dg += RS_THREADS)
+            next[dg] += (dg + 1 < radix ? sm.tot[dg + 1] : cnt) - sm.tot[dg];
         __syncthreads();
     }
 }
@@ -619,7 +684,11 @@ dlrm_status sum_ti(const SumArgs& a, dlrm_dtype dt, cudaStream_t st) {
     return sum_to<TI, __nv_bfloat16>(a, st);
 }
 
+// 16 warps, 1,024 digits, the pairs of a tile
+constexpr size_t SORT_BYTES_MOST = 2 * 16 * 1024 + 4 * 1024 + 128 + 8 * SORT1_MAX;
+
 struct GradLayout {
+    bool one;               // the one-block sort
     int nblocks, passes, bits;
     long long chunk;
     size_t keys[2], vals[2], hist, partial, total;
@@ -629,8 +698,9 @@ GradLayout grad_layout(long long m, int d, long long n) {
     GradLayout L;
     int kb = 1;
     while ((1ll << kb) <= m) ++kb;             // ids 0 .. m
-    L.passes = n <= SORT1_MAX ? 0 : (kb + DIG_BITS_MAX - 1) / DIG_BITS_MAX;
-    L.bits = L.passes ? std::max(4, (kb + L.passes - 1) / L.passes) : 0;
+    L.one = n <= SORT1_MAX;
+    L.passes = (kb + DIG_BITS_MAX - 1) / DIG_BITS_MAX;
+    L.bits = std::max(5, (kb + L.passes - 1) / L.passes);
     const long long tiles = (n + RS_TILE - 1) / RS_TILE;
     const long long per = (tiles + RS_BLOCKS_MAX - 1) / RS_BLOCKS_MAX;
     L.chunk = std::max(1ll, per) * RS_TILE;
@@ -641,10 +711,10 @@ GradLayout grad_layout(long long m, int d, long long n) {
         off = align_up(off + bytes, 256);
         return o;
     };
-    const int pairs = L.passes ? 2 : 1;
+    const int pairs = L.one ? 1 : 2;
     for (int i = 0; i < 2; ++i) L.keys[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
     for (int i = 0; i < 2; ++i) L.vals[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
-    L.hist = take(L.passes ? sizeof(int) * ((size_t)L.nblocks << L.bits) : 0);
+    L.hist = take(!L.one ? sizeof(int) * ((size_t)L.nblocks << L.bits) : 0);
     const long long windows = (n + window_len(n, d) - 1) / window_len(n, d);
     L.partial = take(sizeof(float) * 2 * (size_t)windows * d);
     L.total = off;
@@ -671,8 +741,8 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
     uint32_t* vals[2] = {reinterpret_cast<uint32_t*>(ws + L.vals[0]), reinterpret_cast<uint32_t*>(ws + L.vals[1])};
     int* hist = reinterpret_cast<int*>(ws + L.hist);
     const long long bytes = m * d * (long long)(dT_dt == DLRM_F32 ? 4 : 2);
-    // launches of the sort: a histogram takes about a third of a scatter's time, and so much of the zeros
-    const int shares = L.passes ? 4 * L.passes : 1;
+    // launches of the sort: a histogram takes about a third of a scatter's time, and writes so much of the zeros
+    const int shares = L.one ? 1 : 4 * L.passes;
     long long done = 0;
     auto zeros = [&](int sorters, int share) {
         Zeros z{static_cast<char*>(dT), bytes * done / shares, bytes * (done + share) / shares, sorters};
@@ -684,14 +754,18 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
         return (unsigned)std::max<long long>(1, std::min<long long>((z.end - z.begin + 16383) / 16384, 2ll * device_sms()));
     };
     int cur = 0;
-    if (L.passes == 0) {
-        int padded = 2;
-        while (padded < n) padded <<= 1;
-        const int threads = std::max(256, std::min(1024, padded / 2));
+    if (L.one) {
+        // as many threads as the pairs need at eight each, but enough to write zeros quickly
+        const int threads = n <= 256 * RS_ITEMS ? 256 : SORT1_THREADS;
         const Zeros z = zeros(1, 1);
-        DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1 + writers(z)), dim3(threads),
-                                  sizeof(unsigned long long) * padded, st, (int)n, padded, m, idx, keys[0], vals[0], err, z));
+        const size_t smem = sort_bytes(threads / 32, 1 << L.bits);
+        cudaFuncSetAttribute(sort_one_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SORT_BYTES_MOST);
+        DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1 + writers(z)), dim3(threads), smem, st, (int)n, m, L.passes,
+                                  L.bits, idx, keys[0], vals[0], err, z));
     } else {
+        const size_t smem = sort_bytes(RS_THREADS / 32, 1 << L.bits);
+        cudaFuncSetAttribute(rs_scatter_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SORT_BYTES_MOST);
+        cudaFuncSetAttribute(rs_scatter_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SORT_BYTES_MOST);
         const dim3 block(RS_THREADS);
         for (int p = 0; p < L.passes; ++p) {
             const int shift = p * L.bits;
@@ -700,13 +774,13 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
             if (p == 0) {
                 DLRM_PDL_CHECK(launch_pdl(rs_hist_kernel<true>, gh, block, 0, st, n, m, (const void*)idx, shift,
                                           L.bits, L.chunk, hist, err, zh));
-                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<true>, gs, block, 0, st, n, m, (const void*)idx,
+                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<true>, gs, block, smem, st, n, m, (const void*)idx,
                                           (const uint32_t*)nullptr, shift, L.bits, L.chunk, (const int*)hist,
                                           keys[0], vals[0], zs));
             } else {
                 DLRM_PDL_CHECK(launch_pdl(rs_hist_kernel<false>, gh, block, 0, st, n, m, (const void*)keys[cur], shift,
                                           L.bits, L.chunk, hist, err, zh));
-                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<false>, gs, block, 0, st, n, m, (const void*)keys[cur],
+                DLRM_PDL_CHECK(launch_pdl(rs_scatter_kernel<false>, gs, block, smem, st, n, m, (const void*)keys[cur],
                                           (const uint32_t*)vals[cur], shift, L.bits, L.chunk, (const int*)hist,
                                           keys[cur ^ 1], vals[cur ^ 1], zs));
                 cur ^= 1;

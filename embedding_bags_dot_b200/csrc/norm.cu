@@ -383,8 +383,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(int nparts, int d, con
     __shared__ float part[32][33];
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
     float s = 0.f;
-    if (c < d)
+    if (c < d) {
+#pragma unroll 8
         for (int p = g; p < nparts; p += 32) s += partial[(long long)p * d + c];
+    }
     part[g][threadIdx.x & 31] = s;
     __syncthreads();
     if (g == 0 && c < d) {
@@ -460,23 +462,27 @@ dlrm_status fwd_t(const NormFwdArgs& a, bool q8, cudaStream_t st) {
     return q8 ? fwd_vec<T, 1, true>(a, st) : fwd_vec<T, 1, false>(a, st);
 }
 
-// Most blocks of the backward pass, each of which writes a row of partial sums: about 1,024 threads per SM
-// at two 16-byte runs of a 16-bit type per thread.
-long long bwd_most(int d) { return (long long)device_sms() * std::max(1, std::min(8, 16384 / d)); }
+// Blocks of `threads` threads that are resident at once: 64 registers a thread above 256 threads, 80 below.
+long long bwd_resident(int threads) {
+    return (long long)device_sms() * std::max(1, (threads > 256 ? 1024 : 768) / threads);
+}
+// Most blocks of the backward pass, each of which writes a row of partial sums: those of a 16-bit type, whose rows
+// take the fewest threads.
+long long bwd_most(int d) { return bwd_resident(std::max(96, norm_threads(d, 16))); }
 
 template <typename T, int VEC>
 dlrm_status bwd_vec(const NormBwdArgs& a, int& nblocks, cudaStream_t st) {
     constexpr int W = 16 / (int)sizeof(T);
     constexpr int NV = W / VEC;
     if (norm_threads(a.d, W) == 32) {
-        nblocks = (int)std::min<long long>((a.rows + 3) / 4, bwd_most(a.d));
+        nblocks = (int)std::min<long long>((a.rows + 3) / 4, std::min(bwd_resident(128), bwd_most(a.d)));
         const size_t smem = a.partial ? sizeof(float) * 4 * W * 32 : 0;
         return norm_launch(rmsnorm_bwd_kernel<T, VEC, NV, false, 128, false>, nblocks, 128, smem, a, st);
     }
-    const int two = norm_threads(a.d, 2 * W);
-    nblocks = (int)std::min<long long>(a.rows, bwd_most(a.d));
+    const int two = norm_threads(a.d, 2 * W), wide = norm_threads(a.d, 32);
+    nblocks = (int)std::min<long long>(a.rows, std::min(bwd_resident(two > 1024 ? wide : two), bwd_most(a.d)));
     if (two > 1024)
-        return norm_launch(rmsnorm_bwd_kernel<T, VEC, 32 / VEC, true, 1024, false>, nblocks, norm_threads(a.d, 32), 0, a, st);
+        return norm_launch(rmsnorm_bwd_kernel<T, VEC, 32 / VEC, true, 1024, false>, nblocks, wide, 0, a, st);
     const size_t smem = VEC == W ? (size_t)BWD_RING * 3 * 2 * 16 * two : 0;
     if (two > 256)
         return norm_launch(rmsnorm_bwd_kernel<T, VEC, 2 * NV, true, 1024, VEC == W>, nblocks, two, smem, a, st);
