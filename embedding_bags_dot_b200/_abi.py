@@ -552,14 +552,17 @@ def _vector(t, where: str, dtype, n: int, needed: bool = False):
         if needed:
             _refuse(where)
         return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         _refuse(where)
-    return _ptr(t)
+    return t.data_ptr() if n else None
+
+
+_FLOAT_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
 def _float_code(t, where: str) -> int:
-    code = DT_CODE.get(t.dtype)
-    if code not in (F32, F16, BF16):
+    code = _FLOAT_CODE.get(t.dtype)
+    if code is None:
         _refuse(where)
     return code
 
@@ -576,8 +579,9 @@ def _same_device(where: str, *tensors) -> int:
     return dev
 
 
-def _call(where: str, dev: int, stream, fn, *args):
-    """Runs a C entry point on the tensors' device, which need not be the current one."""
+def _call(where: str, dev: int, stream, *args):
+    """Runs the C entry point `where` on the tensors' device, which need not be the current one."""
+    fn = getattr(_lib or lib(), where)
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif isinstance(stream, torch.cuda.Stream):
@@ -604,7 +608,7 @@ def dlrm_embed_fwd(T: Tables, k: int, indices, out, ws, scale: float = 1.0, stre
     if not 0 <= int(k) < T.K or T.data.numel() < sum(T.rows) * (T.d if T.struct.dt != U8ROW else 1):
         _refuse(f)
     dev = _same_device(f, T.data, indices, out, ws)
-    return _call(f, dev, stream, lib().dlrm_embed_fwd, T.ref(), int(k), n, idx, float(scale), ptr, ld,
+    return _call(f, dev, stream, T.ref(), int(k), n, idx, float(scale), ptr, ld,
                  _float_code(out, f), _ptr(ws), _nbytes(ws))
 
 
@@ -623,7 +627,7 @@ def dlrm_embed_bwd(indices, dout, dtable, ws, scale: float = 1.0, stream=None):
     idx = _vector(indices, f, torch.int32, n)
     ptr, ld = _matrix(dout, f, n, d)
     dev = _same_device(f, indices, dout, dtable, ws)
-    return _call(f, dev, stream, lib().dlrm_embed_bwd, rows, d, n, idx, float(scale), ptr, ld, _float_code(dout, f),
+    return _call(f, dev, stream, rows, d, n, idx, float(scale), ptr, ld, _float_code(dout, f),
                  _ptr(dtable), _float_code(dtable, f), _ptr(ws), _nbytes(ws))
 
 
@@ -638,7 +642,7 @@ def dlrm_dropout(x, y, p: float, rng, residual=None, stream=None):
     args = (_vector(x, f, x.dtype, n), _vector(residual, f, x.dtype, n), _float_code(x, f), float(p),
             _vector(rng, f, torch.int64, 2, True), _vector(y, f, x.dtype, n))
     dev = _same_device(f, x, residual, rng, y)
-    return _call(f, dev, stream, lib().dlrm_dropout, n, *args)
+    return _call(f, dev, stream, n, *args)
 
 
 def dlrm_rmsnorm_fwd(x, w, y, eps: float = 1e-6, residual=None, h=None, y_scale=None, rstd=None, stream=None):
@@ -663,7 +667,7 @@ def dlrm_rmsnorm_fwd(x, w, y, eps: float = 1e-6, residual=None, h=None, y_scale=
     if rows == 0:
         return OK
     dev = _same_device(f, x, w, y, residual, h, y_scale, rstd)
-    return _call(f, dev, stream, lib().dlrm_rmsnorm_fwd, rows, d, px, lx, pr, lr, code, *args)
+    return _call(f, dev, stream, rows, d, px, lx, pr, lr, code, *args)
 
 
 def dlrm_rmsnorm_bwd_workspace_size(rows: int, d: int) -> int:
@@ -684,7 +688,7 @@ def dlrm_rmsnorm_bwd(dy, h, rstd, w, dx, ws, dw=None, dh=None, stream=None):
     args = (_vector(rstd, f, torch.float32, rows, True), _vector(w, f, torch.float32, d), pd, ld, _float_code(dy, f), px,
             lx, _vector(dw, f, torch.float32, d), _ptr(ws), _nbytes(ws))
     dev = _same_device(f, dy, h, rstd, w, dx, dw, dh, ws)
-    return _call(f, dev, stream, lib().dlrm_rmsnorm_bwd, rows, d, py, ly, ph, lh, *args)
+    return _call(f, dev, stream, rows, d, py, ly, ph, lh, *args)
 
 
 def _experts_sizes(X, W, offsets, where: str):
@@ -707,7 +711,7 @@ def dlrm_experts_fwd(X, W, offsets, Y, ws, bias=None, act: int = ACT_NONE, x_sca
     args = (_vector(x_scale, f, torch.float32, M), code, pw, lw, _vector(w_scale, f, torch.float32, n_exp * N),
             _vector(bias, f, torch.float32, n_exp * N), int(act), py, ly, _float_code(Y, f), _ptr(ws), _nbytes(ws))
     dev = _same_device(f, X, W, offsets, Y, ws, bias, x_scale, w_scale)
-    return _call(f, dev, stream, lib().dlrm_experts_fwd, n_exp, M, N, K, offs, px, lx, *args)
+    return _call(f, dev, stream, n_exp, M, N, K, offs, px, lx, *args)
 
 
 def dlrm_experts_bwd_workspace_size(n_experts: int, M: int, N: int, K: int, act: int = ACT_NONE) -> int:
@@ -728,7 +732,7 @@ def dlrm_experts_bwd(dY, X, W, offsets, ws, Y=None, act: int = ACT_NONE, dX=None
             F32 if dX is None else _float_code(dX, f), pdw, ldw, F32 if dW is None else _float_code(dW, f),
             _vector(db, f, torch.float32, n_exp * N), _ptr(ws), _nbytes(ws))
     dev = _same_device(f, dY, X, W, offsets, ws, Y, dX, dW, db)
-    return _call(f, dev, stream, lib().dlrm_experts_bwd, n_exp, M, N, K, offs, *args)
+    return _call(f, dev, stream, n_exp, M, N, K, offs, *args)
 
 
 def grads_view(grads: torch.Tensor, off: int, shape) -> torch.Tensor:
