@@ -18,8 +18,9 @@
 // past row N of W_e reads zeros, not the next expert's weights.
 //
 // Two kernels on tcgen05 with TMA-fed 128-byte-swizzled shared memory:
-//  - expert_pair_kernel: 256 x 256 tiles on SM pairs (cta_group::2), all three
-//    products. Bound by the tensor pipe at large sizes.
+//  - expert_pair_kernel: 256 x 256 tiles on SM pairs (cta_group::2): the forward,
+//    or both products of the backward pass in one launch. Bound by the tensor
+//    pipe at large sizes.
 //  - expert_tile_kernel: tiles of 128 rows and 64 or 128 columns on one SM,
 //    forward only, for calls too small to fill the pairs, where reading the
 //    weights bounds the time. A row block of at most 32 rows loads 32 rows
@@ -57,30 +58,38 @@ struct ExPair {
     static constexpr int OUT = EPI_WARPS * NOUT * STAGE_OUT_BYTES;
 };
 
-enum ExpertOp { EX_FWD = 0, EX_DGRAD = 1, EX_WGRAD = 2 };
+enum ExpertOp { EX_FWD = 0, EX_BWD = 1 };
+enum ExpertTile { ET_FWD = 0, ET_DGRAD = 1, ET_WGRAD = 2 };   // what a tile of the pair kernel computes
 enum ExpertKind { EX_F16 = 0, EX_F8 = 1 };
 
 struct ExpertArgs {
     int E, M;                 // experts; rows of the activations
-    int J;                    // output columns: N (fwd), K (dgrad), K (wgrad)
-    int I;                    // wgrad: output rows per expert (N)
-    int R;                    // reduction length of fwd (K) and dgrad (N)
+    int J;                    // output columns: N (fwd), K (dX and dW)
+    int I;                    // dW: output rows per expert (N), 0 without dW
+    int R;                    // reduction length of fwd (K) and dX (N)
+    bool rows_out;            // whether there is an output with rows (Y, dX)
     const int32_t* offsets;
     bool count;               // whether this launch reports bad ranges
     const float* bias;        // fwd, or null: [E][J]
     const float* x_scale;     // e4m3: [M]
     const float* w_scale;     // e4m3: [E][J]
     bool relu;
-    void* C;
+    void* C;                  // Y or dX
     long long ldc;
     ErrRecord* err;
 };
 
 struct ExpertMaps {
-    CUtensorMap a, b, c;
+    CUtensorMap a, b, c;      // row operand, weights, output with rows
     CUtensorMap a32;          // tile kernel: 32-row boxes of A
-    CUtensorMap at, bt;       // wgrad: zero-padded last blocks
 };
+struct GradMaps {
+    CUtensorMap a, b, c;      // dX: dP, W, dX
+    CUtensorMap wa, wb, wc;   // dW: dP, X, dW
+    CUtensorMap at, bt;       // zero-padded last blocks of dP and X
+};
+template <int OP> struct PairMaps { using t = ExpertMaps; };
+template <> struct PairMaps<EX_BWD> { using t = GradMaps; };
 
 struct Ranges {
     int begin[EX_MAX];
@@ -154,6 +163,23 @@ struct TileWalk {
         }
         return false;
     }
+};
+
+// The pair kernel's list: the tiles of the output with rows first, then those of dW. In one launch, because either
+// alone leaves SMs idle in its last round (270 and 512 tiles over 74 pairs in a batch of 16,384 rows).
+struct TileList {
+    TileWalk rows, mats;
+    bool in_mats = false;
+    long long off = 0;
+    __device__ __forceinline__ bool seek(long long t, int& mb, int& cb) {
+        if (!in_mats) {
+            if (rows.seek(t, mb, cb)) return true;
+            in_mats = true;
+            off = rows.base;
+        }
+        return mats.seek(t - off, mb, cb);
+    }
+    __device__ __forceinline__ int expert() const { return in_mats ? mats.e : rows.e; }
 };
 
 // MN-major 16-bit operand with 128-byte swizzle: each reduction row is 128 bytes (64 consecutive M/N elements),
@@ -263,7 +289,7 @@ struct EpiRow {
 };
 template <int NC, int OP, int KIND>
 __device__ __forceinline__ void ex_fetch(EpiRow<NC>& er, int row0, int nvalid, int j0, int e, const ExpertArgs& a) {
-    if constexpr (OP == EX_FWD) {
+    if constexpr (OP == ET_FWD) {
         const int lane = threadIdx.x & 31;
         er.xs = KIND == EX_F8 && lane < nvalid ? __ldg(a.x_scale + row0 + lane) : 0.f;
 #pragma unroll
@@ -311,7 +337,7 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>&
     for (int c = 0; c < NC / PER; ++c) {
         const int n0 = j0 + c * CW;
         if (n0 >= a.J) break;                   // uniform across the warp
-        if constexpr (OP == EX_FWD) {
+        if constexpr (OP == ET_FWD) {
 #pragma unroll
             for (int p = 0; p < PER; ++p) ex_affine<NC, KIND>(acc[c * PER + p], er, c * PER + p, a);
         }
@@ -340,11 +366,11 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>&
             }
             *reinterpret_cast<uint4*>(row + 16 * (q ^ (lane & 7))) = w;
         }
-        if (OP == EX_WGRAD || nvalid >= 32) {
+        if (OP == ET_WGRAD || nvalid >= 32) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-                if constexpr (OP == EX_WGRAD) ex_store_3d(mapC, stage_s, n0, row0, e);
+                if constexpr (OP == ET_WGRAD) ex_store_3d(mapC, stage_s, n0, row0, e);
                 else tma_store_2d(mapC, stage_s, n0, row0);
             }
         } else {
@@ -372,17 +398,19 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>&
     }
 }
 
-// k-blocks of a tile: the reduction length of fwd and dgrad, the expert's rows in wgrad.
-template <int OP, int KIND>
-__device__ __forceinline__ int ex_kblocks(const ExpertArgs& a, int rows) {
+// k-blocks of a reduction.
+template <int KIND>
+__device__ __forceinline__ int ex_kblocks(int len) {
     constexpr int KE = KIND == EX_F8 ? 128 : 64;
-    return ((OP == EX_WGRAD ? rows : a.R) + KE - 1) / KE;
+    return (len + KE - 1) / KE;
 }
 
-template <typename TC, int OP, int KIND>
+// TC: type of the output with rows; TW: of dW (EX_BWD)
+template <typename TC, typename TW, int OP, int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
-    expert_pair_kernel(const __grid_constant__ ExpertMaps maps, const __grid_constant__ ExpertArgs a, uint32_t id) {
-    constexpr bool AMN = OP == EX_WGRAD, BMN = OP != EX_FWD;
+    expert_pair_kernel(const __grid_constant__ typename PairMaps<OP>::t maps, const __grid_constant__ ExpertArgs a, uint32_t id,
+                       uint32_t id_dw) {
+    constexpr bool BMN = OP != EX_FWD;
     constexpr int KE = KIND == EX_F8 ? 128 : 64;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = su32(smem_raw);
@@ -422,7 +450,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
     const uint32_t tmem = uni(bars->tmem_base);
     volatile int* abort = &bars->abort;
     bool timed_out = false;
-    TileWalk walk{rg, a.E, (a.J + 255) / 256, OP == EX_WGRAD ? 0 : 256, (a.I + 255) / 256};
+    const int nbj = (a.J + 255) / 256;
+    TileList walk{{rg, a.E, a.rows_out ? nbj : 0, 256, 0}, {rg, OP == EX_BWD ? a.E : 0, nbj, 0, (a.I + 255) / 256}};
     int mb, cb;
 
     if (warp < 4) {
@@ -431,8 +460,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
             int s = 0;
             uint32_t ph = 0;
             for (long long t = pair; !timed_out && uni(walk.seek(t, mb, cb)); t += npair) {
-                const int e = uni(walk.e), r0 = uni(rg->begin[e]), rows = uni(rg->end[e]) - r0;
-                const int nk = ex_kblocks<OP, KIND>(a, rows);
+                const int e = uni(walk.expert()), r0 = uni(rg->begin[e]), rows = uni(rg->end[e]) - r0;
+                const bool dw = OP == EX_BWD && uni(walk.in_mats);
+                const int nk = ex_kblocks<KIND>(dw ? rows : a.R);
                 const int arow = uni(mb) * 256 + (int)rank * 128, brow = uni(cb) * 256 + (int)rank * 128;
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&bars->empty[s], ph ^ 1u, abort))) {
@@ -443,28 +473,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
                     const uint32_t bar = map_rank(su32(&bars->full[s]), 0);
                     if (elect_one()) {
                         if (leader) mbar_expect_tx(&bars->full[s], 2 * EX_STAGE2_BYTES);
-                        if constexpr (OP == EX_WGRAD) {
-                            if (kb * KE + KE <= rows) {
+                        if constexpr (OP == EX_FWD) {
+                            tma_load_2d_pair(sa, &maps.a, bar, kb * KE, r0 + arow);
+                            ex_load_3d_pair(sb, &maps.b, bar, kb * KE, brow, e);
+                        } else if (!dw) {
+                            tma_load_2d_pair(sa, &maps.a, bar, kb * KE, r0 + arow);
 #pragma unroll
-                                for (int b = 0; b < 2; ++b) {
-                                    tma_load_2d_pair(sa + b * 8192, &maps.a, bar, arow + 64 * b, r0 + kb * KE);
-                                    tma_load_2d_pair(sb + b * 8192, &maps.b, bar, brow + 64 * b, r0 + kb * KE);
-                                }
-                            } else {
+                            for (int b = 0; b < 2; ++b)
+                                ex_load_3d_pair(sb + b * 8192, &maps.b, bar, brow + 64 * b, kb * KE, e);
+                        } else if (kb * KE + KE <= rows) {
 #pragma unroll
-                                for (int b = 0; b < 2; ++b) {
-                                    ex_load_3d_pair(sa + b * 8192, &maps.at, bar, arow + 64 * b, 0, e);
-                                    ex_load_3d_pair(sb + b * 8192, &maps.bt, bar, brow + 64 * b, 0, e);
-                                }
+                            for (int b = 0; b < 2; ++b) {
+                                tma_load_2d_pair(sa + b * 8192, &maps.wa, bar, arow + 64 * b, r0 + kb * KE);
+                                tma_load_2d_pair(sb + b * 8192, &maps.wb, bar, brow + 64 * b, r0 + kb * KE);
                             }
                         } else {
-                            tma_load_2d_pair(sa, &maps.a, bar, kb * KE, r0 + arow);
-                            if constexpr (OP == EX_FWD) {
-                                ex_load_3d_pair(sb, &maps.b, bar, kb * KE, brow, e);
-                            } else {
 #pragma unroll
-                                for (int b = 0; b < 2; ++b)
-                                    ex_load_3d_pair(sb + b * 8192, &maps.b, bar, brow + 64 * b, kb * KE, e);
+                            for (int b = 0; b < 2; ++b) {
+                                ex_load_3d_pair(sa + b * 8192, &maps.at, bar, arow + 64 * b, 0, e);
+                                ex_load_3d_pair(sb + b * 8192, &maps.bt, bar, brow + 64 * b, 0, e);
                             }
                         }
                     }
@@ -487,14 +514,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
             }
         } else if (warp == 1) {
             if (leader) {
-                const uint64_t a0 = AMN ? sdesc_mn16(base) : sdesc(base);
+                const uint64_t ak = sdesc(base), am = sdesc_mn16(base);      // A of rows, A of dW
                 const uint64_t b0 = BMN ? sdesc_mn16(base + EX_STAGE2_BYTES / 2) : sdesc(base + EX_STAGE2_BYTES / 2);
-                const uint32_t ahi = (uint32_t)(a0 >> 32), bhi = (uint32_t)(b0 >> 32);
-                constexpr uint32_t ASTEP = (AMN ? 2048 : 32) >> 4, BSTEP = (BMN ? 2048 : 32) >> 4;   // one MMA's depth
+                const uint32_t bhi = (uint32_t)(b0 >> 32);
+                constexpr uint32_t BSTEP = (BMN ? 2048 : 32) >> 4;           // one MMA's depth
                 int s = 0;
                 uint32_t ph = 0, part = 0;   // accumulator parts so far: part n uses TMEM buffer n & 1
                 for (long long t = pair; !timed_out && uni(walk.seek(t, mb, cb)); t += npair) {
-                    const int nk = uni(ex_kblocks<OP, KIND>(a, rg->end[walk.e] - rg->begin[walk.e]));
+                    const int e = walk.expert();
+                    const bool dw = OP == EX_BWD && uni(walk.in_mats);
+                    const int nk = uni(ex_kblocks<KIND>(dw ? rg->end[e] - rg->begin[e] : a.R));
+                    const uint64_t a0 = dw ? am : ak;
+                    const uint32_t ahi = (uint32_t)(a0 >> 32), astep = (dw ? 2048 : 32) >> 4, idt = dw ? id_dw : id;
                     for (int kb = 0; kb < nk; ++kb) {
                         const uint32_t acc = part & 1u;
                         bool ok = true;
@@ -512,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                ex_umma<KIND, 2>(d, desc64(ahi, alo + k * ASTEP), desc64(bhi, blo + k * BSTEP), id,
+                                ex_umma<KIND, 2>(d, desc64(ahi, alo + k * astep), desc64(bhi, blo + k * BSTEP), idt,
                                                  ((kb % PART) | k) != 0);
                             umma2_commit_both(&bars->empty[s]);
                             if (last) umma2_commit_both(&bars->tfull[acc]);
@@ -542,13 +573,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
         const uint32_t lead_tempty1 = map_rank(su32(&bars->tempty[1]), 0);
         uint32_t part = 0;
         for (long long t = pair; !timed_out && walk.seek(t, mb, cb); t += npair) {
-            const int e = walk.e, r0 = rg->begin[e], rows = rg->end[e] - r0;
-            const int parts = (ex_kblocks<OP, KIND>(a, rows) + PART - 1) / PART;
+            const int e = walk.expert(), r0 = rg->begin[e], rows = rg->end[e] - r0;
+            const bool dw = OP == EX_BWD && walk.in_mats;
+            const int parts = (ex_kblocks<KIND>(dw ? rows : a.R) + PART - 1) / PART;
             const int in_tile = mb * 256 + (int)rank * 128 + q * 32, j0 = cb * 256 + h * 128;
-            const int row0 = OP == EX_WGRAD ? in_tile : r0 + in_tile;
-            const int nvalid = (OP == EX_WGRAD ? a.I : rows) - in_tile;
+            const int row0 = dw ? in_tile : r0 + in_tile;
+            const int nvalid = (dw ? a.I : rows) - in_tile;
             EpiRow<4> er;
-            ex_fetch<4, OP, KIND>(er, row0, nvalid, j0, e, a);
+            if constexpr (OP == EX_FWD) ex_fetch<4, ET_FWD, KIND>(er, row0, nvalid, j0, e, a);
             float acc[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -567,7 +599,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
                 if (lane == 0) mbar_arrive_cluster(b ? lead_tempty1 : lead_tempty0);
             }
             if (timed_out) break;
-            ex_store<TC, 4, OP, KIND, P::NOUT>(acc, er, row0, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
+            if constexpr (OP == EX_FWD) {
+                ex_store<TC, 4, ET_FWD, KIND, P::NOUT>(acc, er, row0, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
+            } else if (dw) {
+                ex_store<TW, 4, ET_WGRAD, KIND, P::NOUT>(acc, er, row0, nvalid, j0, e, a, &maps.wc, stage, stage_s, buf);
+            } else {
+                ex_store<TC, 4, ET_DGRAD, KIND, P::NOUT>(acc, er, row0, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
+            }
         }
         if (timed_out) *abort = 1;
         if (lane == 0) bulk_wait_all0();
@@ -605,7 +643,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     Ranges* rg = reinterpret_cast<Ranges*>(gbase + NS * T::STAGE + OUT_BYTES);
     ExBars<NS>* bars = reinterpret_cast<ExBars<NS>*>(rg + 1);
     const int warp = uni(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int nk = ex_kblocks<EX_FWD, KIND>(a, 0);
+    const int nk = ex_kblocks<KIND>(a.R);
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bars->full[s], 1);
@@ -727,7 +765,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool some = active && row < rg->end[e];
             const int nvalid = active ? rg->end[e] - row : 0, j0 = cb * BNT + h * T::WC;
             EpiRow<NC> er;
-            ex_fetch<NC, EX_FWD, KIND>(er, row, nvalid, j0, e, a);
+            ex_fetch<NC, ET_FWD, KIND>(er, row, nvalid, j0, e, a);
             float acc[NC][32];
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -746,7 +784,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(&bars->tempty[b]);
             }
             if (timed_out) break;
-            if (some) ex_store<TC, NC, EX_FWD, KIND, 1>(acc, er, row, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
+            if (some) ex_store<TC, NC, ET_FWD, KIND, 1>(acc, er, row, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
         }
         if (timed_out) *abort = 1;
         if (lane == 0) bulk_wait_all0();
@@ -788,6 +826,7 @@ struct PrepArgs {
 
 constexpr int PREP_ROWS = 64;     // rows per chunk: one reduction block of wgrad
 constexpr int PREP_COLS = 8;      // columns per thread: 16 bytes
+constexpr int PREP_THREADS = 128;
 
 // The expert and first row of chunk number `chunk` (experts in order, each cut into 64-row chunks from its first
 // row), found by the whole block's first warp; e = E if there is no such chunk.
@@ -827,9 +866,9 @@ __device__ __forceinline__ void load_run(RowRaw<T, PREP_COLS>& v, const T* p, in
     }
 }
 
-// Block (chunk, slice): up to 64 rows x 256 * 8 columns, one run of 8 columns per thread.
+// Block (chunk, slice): up to 64 rows x 128 * 8 columns, one run of 8 columns per thread.
 template <typename T>
-__global__ void __launch_bounds__(256) expert_prep_kernel(const __grid_constant__ PrepArgs a) {
+__global__ void __launch_bounds__(PREP_THREADS) expert_prep_kernel(const __grid_constant__ PrepArgs a) {
     pdl_wait();
     __shared__ Ranges rg;
     __shared__ int se;
@@ -847,7 +886,7 @@ __global__ void __launch_bounds__(256) expert_prep_kernel(const __grid_constant_
     const bool tail = rows < PREP_ROWS;
     if ((int)blockIdx.y >= a.nslices) {
         // X: only the padded copy of a last block
-        const long long c = ((long long)(blockIdx.y - a.nslices) * 256 + threadIdx.x) * PREP_COLS;
+        const long long c = ((long long)(blockIdx.y - a.nslices) * PREP_THREADS + threadIdx.x) * PREP_COLS;
         if (!tail || !a.tail_x || c >= a.K) return;
         const T* x = static_cast<const T*>(a.X) + r0 * a.ldx + c;
         T* out = static_cast<T*>(a.tail_x) + (long long)e * PREP_ROWS * a.ldtx + c;
@@ -860,7 +899,7 @@ __global__ void __launch_bounds__(256) expert_prep_kernel(const __grid_constant_
         }
         return;
     }
-    const long long c = ((long long)blockIdx.y * 256 + threadIdx.x) * PREP_COLS;
+    const long long c = ((long long)blockIdx.y * PREP_THREADS + threadIdx.x) * PREP_COLS;
     if (c >= a.N) return;
     const bool mask = a.Y != nullptr;
     if (!mask && !a.part && !(tail && a.tail_dp)) return;
@@ -921,7 +960,7 @@ __global__ void __launch_bounds__(256) expert_bias_kernel(const __grid_constant_
     __shared__ float share[8][33];
     const int e = blockIdx.y;
     if (threadIdx.x < 32) {
-        read_ranges(a, &rg, false);
+        read_ranges(a, &rg, a.count && blockIdx.x == 0 && e == 0);
         __syncwarp();
         long long s = 0;
         for (int q = threadIdx.x; q < e; q += 32) s += (rg.end[q] - rg.begin[q] + PREP_ROWS - 1) / PREP_ROWS;
@@ -979,13 +1018,14 @@ long long most_tiles(int E, long long M, int rows_per, long long nb) {
     return (M / rows_per + std::min<long long>(E, M)) * nb;
 }
 
-template <typename TC, int OP, int KIND>
-dlrm_status launch_pair(const ExpertMaps& maps, const ExpertArgs& a, uint32_t id, long long tiles, cudaStream_t st) {
-    auto kern = expert_pair_kernel<TC, OP, KIND>;
+template <typename TC, typename TW, int OP, int KIND>
+dlrm_status launch_pair(const typename PairMaps<OP>::t& maps, const ExpertArgs& a, uint32_t id, uint32_t id_dw,
+                        long long tiles, cudaStream_t st) {
+    auto kern = expert_pair_kernel<TC, TW, OP, KIND>;
     cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, EX_SMEM2<KIND>);
     const int pairs = device_sms() / 2;
     const dim3 grid((unsigned)(2 * std::min<long long>(tiles, pairs)));
-    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(EX_THREADS2), (size_t)EX_SMEM2<KIND>, st, maps, a, id));
+    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(EX_THREADS2), (size_t)EX_SMEM2<KIND>, st, maps, a, id, id_dw));
     return DLRM_OK;
 }
 
@@ -1010,7 +1050,7 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
                                cudaStream_t st) {
     using namespace tc;
     const int es = ex_size(dt), ke = 128 / es;
-    ExpertArgs a{E, M, N, 0, K, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, err};
+    const ExpertArgs a{E, M, N, 0, K, true, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, err};
     // SM pairs once their 256 x 256 tiles can fill them (rows spread evenly over the experts). Otherwise one SM per
     // tile: 64 columns wide if that gives every tile an SM of its own, else 128 (12 rows of 8 experts, 4,096 x 1,024
     // bf16: 13.6 us at 128, 15.5 at 64, 17.6 at 32; a k-block's issue costs 420 to 465 cycles at any width).
@@ -1028,8 +1068,8 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
         return DLRM_ERR_CUDA;
     const int fmt = dt == DLRM_BF16 ? 1 : 0;
 #define DLRM_EX_FWD(TC, KIND)                                                                     \
-    return pair ? launch_pair<TC, EX_FWD, KIND>(maps, a, ex_idesc(fmt, false, false, 256, 256),   \
-                                                most_tiles(E, M, 256, nb2), st)                   \
+    return pair ? launch_pair<TC, TC, EX_FWD, KIND>(maps, a, ex_idesc(fmt, false, false, 256, 256), \
+                                                    0u, most_tiles(E, M, 256, nb2), st)           \
            : narrow ? launch_tile<TC, KIND, 64>(maps, a, fmt, st)                                 \
                     : launch_tile<TC, KIND, 128>(maps, a, fmt, st);
     if (dt == DLRM_E4M3) {
@@ -1069,16 +1109,16 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
     const bool relu = Y != nullptr;
     const ExpertsLayout L = experts_layout(E, M, N, K, relu);
     ErrRecord* err = reinterpret_cast<ErrRecord*>(ws);
-    ExpertArgs base{E, M, 0, 0, 0, offsets, true, nullptr, nullptr, nullptr, false, nullptr, 0, err};
+    ExpertArgs a{E, M, K, dW ? N : 0, N, dX != nullptr, offsets, true, nullptr, nullptr, nullptr, false, dX, lddx, err};
     float* part = reinterpret_cast<float*>(ws + L.part);
     const void* dP = relu ? (const void*)(ws + L.dp) : dY;
     const long long ldp = relu ? L.ldp : lddy;
     if (M > 0 && (relu || db || dW)) {
         PrepArgs p{};
-        p.x = base;
+        p.x = a;
         p.N = N;
         p.K = K;
-        const int per = 256 * PREP_COLS;
+        const int per = PREP_THREADS * PREP_COLS;
         p.nslices = (N + per - 1) / per;
         const int xs = dW ? (K + per - 1) / per : 0;
         p.dY = dY;
@@ -1094,58 +1134,53 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
         p.tail_x = dW ? ws + L.tail_x : nullptr;
         p.ldtx = L.ldtx;
         const dim3 grid((unsigned)(M / PREP_ROWS + std::min(E, M)), p.nslices + xs);
-        if (dt == DLRM_BF16) DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, p));
-        else DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__half>, grid, dim3(256), 0, st, p));
-        base.count = false;
+        if (dt == DLRM_BF16) DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__nv_bfloat16>, grid, dim3(PREP_THREADS), 0, st, p));
+        else DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__half>, grid, dim3(PREP_THREADS), 0, st, p));
+        a.count = false;
     }
     if (db) {
-        DLRM_PDL_CHECK(launch_pdl(expert_bias_kernel, dim3((N + 31) / 32, E), dim3(256), 0, st, base, N,
+        DLRM_PDL_CHECK(launch_pdl(expert_bias_kernel, dim3((N + 31) / 32, E), dim3(256), 0, st, a, N,
                                   (const float*)part, db));
+        a.count = false;
     }
-    const int fmt = dt == DLRM_BF16 ? 1 : 0;
-    if (dX && M > 0) {
-        ExpertArgs a = base;
-        a.J = K;
-        a.R = N;
-        a.C = dX;
-        a.ldc = lddx;
-        ExpertMaps maps{};
+    if ((!dX || M == 0) && !dW) return DLRM_OK;
+    GradMaps maps{};
+    const long long nbk = (K + 255) / 256;
+    long long tiles = 0;
+    a.rows_out = dX && M > 0;
+    if (a.rows_out) {
         if (!ex_map(&maps.a, dP, 2, dt, 2, N, M, 1, ldp, 64, 128) || !ex_map(&maps.b, W, 2, dt, 3, K, N, E, ldw, 64, 64) ||
             !ex_map(&maps.c, dX, ex_size(dx_dt), dx_dt, 2, K, M, 1, lddx, 128 / ex_size(dx_dt), 32))
             return DLRM_ERR_CUDA;
-        const long long tiles = most_tiles(E, M, 256, (K + 255) / 256);
-        const uint32_t id = ex_idesc(fmt, false, true, 256, 256);
-        const dlrm_status r = dx_dt == DLRM_F32    ? launch_pair<float, EX_DGRAD, EX_F16>(maps, a, id, tiles, st)
-                              : dx_dt == DLRM_BF16 ? launch_pair<__nv_bfloat16, EX_DGRAD, EX_F16>(maps, a, id, tiles, st)
-                                                   : launch_pair<__half, EX_DGRAD, EX_F16>(maps, a, id, tiles, st);
-        if (r != DLRM_OK) return r;
-        base.count = false;
+        tiles += most_tiles(E, M, 256, nbk);
     }
     if (dW) {
-        ExpertArgs a = base;
-        a.I = N;
-        a.J = K;
-        a.C = dW;
-        a.ldc = lddw;
-        ExpertMaps maps{};
         // without rows nothing is loaded; the maps still need an address
         const void* pa = M > 0 ? dP : ws + L.tail_dp;
         const void* pb = M > 0 ? X : ws + L.tail_x;
         const long long rows = M > 0 ? M : 1;
-        if (!ex_map(&maps.a, pa, 2, dt, 2, N, rows, 1, M > 0 ? ldp : L.ldp, 64, 64) ||
-            !ex_map(&maps.b, pb, 2, dt, 2, K, rows, 1, M > 0 ? ldx : L.ldtx, 64, 64) ||
+        if (!ex_map(&maps.wa, pa, 2, dt, 2, N, rows, 1, M > 0 ? ldp : L.ldp, 64, 64) ||
+            !ex_map(&maps.wb, pb, 2, dt, 2, K, rows, 1, M > 0 ? ldx : L.ldtx, 64, 64) ||
             !ex_map(&maps.at, ws + L.tail_dp, 2, dt, 3, N, PREP_ROWS, E, L.ldp, 64, 64) ||
             !ex_map(&maps.bt, ws + L.tail_x, 2, dt, 3, K, PREP_ROWS, E, L.ldtx, 64, 64) ||
-            !ex_map(&maps.c, dW, ex_size(dw_dt), dw_dt, 3, K, N, E, lddw, 128 / ex_size(dw_dt), 32))
+            !ex_map(&maps.wc, dW, ex_size(dw_dt), dw_dt, 3, K, N, E, lddw, 128 / ex_size(dw_dt), 32))
             return DLRM_ERR_CUDA;
-        const long long tiles = (long long)E * ((N + 255) / 256) * ((K + 255) / 256);
-        const uint32_t id = ex_idesc(fmt, true, true, 256, 256);
-        const dlrm_status r = dw_dt == DLRM_F32    ? launch_pair<float, EX_WGRAD, EX_F16>(maps, a, id, tiles, st)
-                              : dw_dt == DLRM_BF16 ? launch_pair<__nv_bfloat16, EX_WGRAD, EX_F16>(maps, a, id, tiles, st)
-                                                   : launch_pair<__half, EX_WGRAD, EX_F16>(maps, a, id, tiles, st);
-        if (r != DLRM_OK) return r;
+        tiles += (long long)E * ((N + 255) / 256) * nbk;
     }
-    return DLRM_OK;
+    const int fmt = dt == DLRM_BF16 ? 1 : 0;
+    const uint32_t id = ex_idesc(fmt, false, true, 256, 256), id_dw = ex_idesc(fmt, true, true, 256, 256);
+    // an output that is not asked for takes the other's type
+    const bool fx = dX ? dx_dt == DLRM_F32 : dw_dt == DLRM_F32, fw = dW ? dw_dt == DLRM_F32 : fx;
+#define DLRM_EX_BWD(T)                                                                                               \
+    return fx && fw ? launch_pair<float, float, EX_BWD, EX_F16>(maps, a, id, id_dw, tiles, st)                       \
+           : fx     ? launch_pair<float, T, EX_BWD, EX_F16>(maps, a, id, id_dw, tiles, st)                           \
+           : fw     ? launch_pair<T, float, EX_BWD, EX_F16>(maps, a, id, id_dw, tiles, st)                           \
+                    : launch_pair<T, T, EX_BWD, EX_F16>(maps, a, id, id_dw, tiles, st);
+    if (dt == DLRM_BF16) {
+        DLRM_EX_BWD(__nv_bfloat16)
+    }
+    DLRM_EX_BWD(__half)
+#undef DLRM_EX_BWD
 }
 
 bool experts_supported() { return tc::encode_fn() != nullptr; }

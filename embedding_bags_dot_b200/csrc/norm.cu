@@ -376,23 +376,32 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : MAXT == 256 ? 3 : 4) 
     }
 }
 
-// dw[c] = sum over blocks of partial[block][c]: 32 columns a block, 32 row groups, all in fixed order.
+// dw[c] = sum over blocks of partial[block][c]: 16 columns a block, 64 row groups, all in fixed order.
 __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(int nparts, int d, const float* __restrict__ partial,
                                                           float* __restrict__ dw) {
     pdl_wait();
-    __shared__ float part[32][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+    __shared__ float part[64][17];
+    const int lane = threadIdx.x & 15, g = threadIdx.x >> 4, c = blockIdx.x * 16 + lane;
     float s = 0.f;
     if (c < d) {
 #pragma unroll 8
-        for (int p = g; p < nparts; p += 32) s += partial[(long long)p * d + c];
+        for (int p = g; p < nparts; p += 64) s += partial[(long long)p * d + c];
     }
-    part[g][threadIdx.x & 31] = s;
+    part[g][lane] = s;
+    __syncthreads();
+    // eight sums of eight groups, then one of those
+    if (g < 8) {
+        s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += part[g * 8 + q][lane];
+    }
+    __syncthreads();
+    if (g < 8) part[g][lane] = s;
     __syncthreads();
     if (g == 0 && c < d) {
         s = 0.f;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) s += part[q][threadIdx.x];
+        for (int q = 0; q < 8; ++q) s += part[q][lane];
         dw[c] = s;
     }
 }
@@ -530,7 +539,7 @@ dlrm_status launch_rmsnorm_bwd(int rows, int d, const void* dy, long long lddy, 
                                                : bwd_t<__nv_bfloat16>(a, nblocks, st);
         if (r != DLRM_OK) return r;
     }
-    if (dw) DLRM_PDL_CHECK(launch_pdl(rmsnorm_dw_kernel, dim3((d + 31) / 32), dim3(1024), 0, st, nblocks, d,
+    if (dw) DLRM_PDL_CHECK(launch_pdl(rmsnorm_dw_kernel, dim3((d + 15) / 16), dim3(1024), 0, st, nblocks, d,
                                       (const float*)partial, dw));
     return DLRM_OK;
 }
