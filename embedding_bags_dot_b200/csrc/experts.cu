@@ -826,7 +826,8 @@ struct PrepArgs {
 
 constexpr int PREP_ROWS = 64;     // rows per chunk: one reduction block of wgrad
 constexpr int PREP_COLS = 8;      // columns per thread: 16 bytes
-constexpr int PREP_THREADS = 128;
+constexpr int PREP_RUNS = 64;     // column runs of a block: 512 columns, each run by four threads of 16 rows
+constexpr int PREP_SPAN = PREP_RUNS * PREP_COLS;
 
 // The expert and first row of chunk number `chunk` (experts in order, each cut into 64-row chunks from its first
 // row), found by the whole block's first warp; e = E if there is no such chunk.
@@ -866,88 +867,93 @@ __device__ __forceinline__ void load_run(RowRaw<T, PREP_COLS>& v, const T* p, in
     }
 }
 
-// Block (chunk, slice): up to 64 rows x 128 * 8 columns, one run of 8 columns per thread.
+// Blocks take (chunk, slice) after (chunk, slice): up to 64 rows x 512 columns. Thread (run, quarter) has a run of
+// 8 columns of 16 rows, so that a chunk takes two rounds of eight loads, not sixteen of four; the quarters' column
+// sums are added in order.
 template <typename T>
-__global__ void __launch_bounds__(PREP_THREADS) expert_prep_kernel(const __grid_constant__ PrepArgs a) {
+__global__ void __launch_bounds__(256) expert_prep_kernel(const __grid_constant__ PrepArgs a) {
     pdl_wait();
     __shared__ Ranges rg;
     __shared__ int se;
     __shared__ long long sj;
-    if (threadIdx.x < 32) {
-        read_ranges(a.x, &rg, a.x.count && blockIdx.x == 0 && blockIdx.y == 0);
-        __syncwarp();
-        find_chunk(&rg, a.x.E, blockIdx.x, &se, &sj);
-    }
-    __syncthreads();
-    const int e = se;
-    if (e >= a.x.E) return;
-    const long long r0 = rg.begin[e] + sj * PREP_ROWS;
-    const int rows = (int)(rg.end[e] - r0 < PREP_ROWS ? rg.end[e] - r0 : PREP_ROWS);
-    const bool tail = rows < PREP_ROWS;
-    if ((int)blockIdx.y >= a.nslices) {
-        // X: only the padded copy of a last block
-        const long long c = ((long long)(blockIdx.y - a.nslices) * PREP_THREADS + threadIdx.x) * PREP_COLS;
-        if (!tail || !a.tail_x || c >= a.K) return;
-        const T* x = static_cast<const T*>(a.X) + r0 * a.ldx + c;
-        T* out = static_cast<T*>(a.tail_x) + (long long)e * PREP_ROWS * a.ldtx + c;
-        const int valid = a.K - c < PREP_COLS ? (int)(a.K - c) : PREP_COLS;
-        for (int r = 0; r < PREP_ROWS; ++r) {
-            RowRaw<T, PREP_COLS> v;
-            if (r < rows) load_run(v, x + r * a.ldx, valid);
-            else v.zero();
-            v.store(out + r * a.ldtx);
-        }
-        return;
-    }
-    const long long c = ((long long)blockIdx.y * PREP_THREADS + threadIdx.x) * PREP_COLS;
-    if (c >= a.N) return;
+    __shared__ float quarter[3][PREP_RUNS][PREP_COLS + 1];
+    if (threadIdx.x < 32) read_ranges(a.x, &rg, a.x.count && blockIdx.x == 0 && blockIdx.y == 0);
+    const bool is_x = (int)blockIdx.y >= a.nslices;
+    const int run = threadIdx.x % PREP_RUNS, q = threadIdx.x / PREP_RUNS;
+    const long long c = (is_x ? blockIdx.y - a.nslices : blockIdx.y) * (long long)PREP_SPAN + run * PREP_COLS;
+    const long long width = is_x ? a.K : a.N;
+    const int valid = width - c >= PREP_COLS ? PREP_COLS : width > c ? (int)(width - c) : 0;
     const bool mask = a.Y != nullptr;
-    if (!mask && !a.part && !(tail && a.tail_dp)) return;
-    const T* dy = static_cast<const T*>(a.dY) + r0 * a.lddy + c;
-    const T* y = mask ? static_cast<const T*>(a.Y) + r0 * a.ldyy + c : nullptr;
-    T* dp = mask ? static_cast<T*>(a.dP) + r0 * a.ldp + c : nullptr;
-    T* tl = tail && a.tail_dp ? static_cast<T*>(a.tail_dp) + (long long)e * PREP_ROWS * a.ldp + c : nullptr;
-    const int valid = a.N - c < PREP_COLS ? (int)(a.N - c) : PREP_COLS;
-    float sum[PREP_COLS];
+    for (long long chunk = blockIdx.x;; chunk += gridDim.x) {
+        __syncthreads();
+        if (threadIdx.x < 32) find_chunk(&rg, a.x.E, chunk, &se, &sj);
+        __syncthreads();
+        const int e = se;
+        if (e >= a.x.E) return;
+        const long long r0 = rg.begin[e] + sj * PREP_ROWS;
+        const int rows = (int)(rg.end[e] - r0 < PREP_ROWS ? rg.end[e] - r0 : PREP_ROWS);
+        const bool tail = rows < PREP_ROWS && a.tail_dp;
+        // X only has its last, incomplete blocks copied; so has dY where neither ReLU nor bias sums are wanted
+        if (is_x || (!mask && !a.part))
+            if (!tail) continue;
+        const T* src = is_x ? static_cast<const T*>(a.X) + r0 * a.ldx + c : static_cast<const T*>(a.dY) + r0 * a.lddy + c;
+        const long long ld = is_x ? a.ldx : a.lddy, ldt = is_x ? a.ldtx : a.ldp;
+        const T* y = mask && !is_x ? static_cast<const T*>(a.Y) + r0 * a.ldyy + c : nullptr;
+        T* dp = mask && !is_x ? static_cast<T*>(a.dP) + r0 * a.ldp + c : nullptr;
+        T* tl = tail ? static_cast<T*>(is_x ? a.tail_x : a.tail_dp) + (long long)e * PREP_ROWS * ldt + c : nullptr;
+        float sum[PREP_COLS];
 #pragma unroll
-    for (int k = 0; k < PREP_COLS; ++k) sum[k] = 0.f;
-    constexpr int U = 4;
-    for (int r = 0; r < rows; r += U) {
-        RowRaw<T, PREP_COLS> g[U], f[U];
+        for (int k = 0; k < PREP_COLS; ++k) sum[k] = 0.f;
+        constexpr int U = 8, PER = PREP_ROWS / 4;
+        if (valid > 0) {
+#pragma unroll 1
+            for (int i = 0; i < PER; i += U) {
+                RowRaw<T, PREP_COLS> g[U], f[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (r + u < rows) {
-                load_run(g[u], dy + (long long)(r + u) * a.lddy, valid);
-                if (mask) load_run(f[u], y + (long long)(r + u) * a.ldyy, valid);
-            }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (r + u < rows) {
-                float v[PREP_COLS];
-                g[u].get(v);
-                if (mask) {
-                    float o[PREP_COLS];
-                    f[u].get(o);
-#pragma unroll
-                    for (int k = 0; k < PREP_COLS; ++k)
-                        if (!(o[k] > 0.f)) v[k] = 0.f;
-                    g[u].set(v);
-                    g[u].store(dp + (long long)(r + u) * a.ldp);
+                for (int u = 0; u < U; ++u) {
+                    const int r = q * PER + i + u;
+                    if (r < rows) {
+                        load_run(g[u], src + r * ld, valid);
+                        if (y) load_run(f[u], y + r * a.ldyy, valid);
+                    } else {
+                        g[u].zero();
+                    }
                 }
-                if (tl) g[u].store(tl + (long long)(r + u) * a.ldp);
 #pragma unroll
-                for (int k = 0; k < PREP_COLS; ++k) sum[k] += v[k];
+                for (int u = 0; u < U; ++u) {
+                    const int r = q * PER + i + u;
+                    float v[PREP_COLS];
+                    g[u].get(v);
+                    if (y && r < rows) {
+                        float o[PREP_COLS];
+                        f[u].get(o);
+#pragma unroll
+                        for (int k = 0; k < PREP_COLS; ++k)
+                            if (!(o[k] > 0.f)) v[k] = 0.f;
+                        g[u].set(v);
+                        g[u].store(dp + r * a.ldp);
+                    }
+                    if (tl) g[u].store(tl + r * ldt);       // rows past the last are the zeros
+#pragma unroll
+                    for (int k = 0; k < PREP_COLS; ++k) sum[k] += v[k];
+                }
             }
-    }
-    if (tl) {
-        RowRaw<T, PREP_COLS> z;
-        z.zero();
-        for (int r = rows; r < PREP_ROWS; ++r) z.store(tl + (long long)r * a.ldp);
-    }
-    if (a.part) {
+        }
+        if (!a.part || is_x) continue;
+        if (q > 0) {
 #pragma unroll
-        for (int k = 0; k < PREP_COLS; ++k)
-            if (c + k < a.N) a.part[(long long)blockIdx.x * a.N + c + k] = sum[k];
+            for (int k = 0; k < PREP_COLS; ++k) quarter[q - 1][run][k] = sum[k];
+        }
+        __syncthreads();
+        if (q == 0) {
+#pragma unroll
+            for (int k = 0; k < PREP_COLS; ++k) {
+                float s = sum[k];
+#pragma unroll
+                for (int p = 0; p < 3; ++p) s += quarter[p][run][k];
+                if (k < valid) a.part[chunk * a.N + c + k] = s;
+            }
+        }
     }
 }
 
@@ -1118,9 +1124,8 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
         p.x = a;
         p.N = N;
         p.K = K;
-        const int per = PREP_THREADS * PREP_COLS;
-        p.nslices = (N + per - 1) / per;
-        const int xs = dW ? (K + per - 1) / per : 0;
+        p.nslices = (N + PREP_SPAN - 1) / PREP_SPAN;
+        const int xs = dW ? (K + PREP_SPAN - 1) / PREP_SPAN : 0;
         p.dY = dY;
         p.lddy = lddy;
         p.Y = Y;
@@ -1133,9 +1138,11 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
         p.tail_dp = dW ? ws + L.tail_dp : nullptr;
         p.tail_x = dW ? ws + L.tail_x : nullptr;
         p.ldtx = L.ldtx;
-        const dim3 grid((unsigned)(M / PREP_ROWS + std::min(E, M)), p.nslices + xs);
-        if (dt == DLRM_BF16) DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__nv_bfloat16>, grid, dim3(PREP_THREADS), 0, st, p));
-        else DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__half>, grid, dim3(PREP_THREADS), 0, st, p));
+        // at most six blocks per SM, each of which looks up its ranges once
+        const int chunks = M / PREP_ROWS + std::min(E, M), slices = p.nslices + xs;
+        const dim3 grid((unsigned)std::min(chunks, std::max(1, 6 * device_sms() / slices)), slices);
+        if (dt == DLRM_BF16) DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, p));
+        else DLRM_PDL_CHECK(launch_pdl(expert_prep_kernel<__half>, grid, dim3(256), 0, st, p));
         a.count = false;
     }
     if (db) {
