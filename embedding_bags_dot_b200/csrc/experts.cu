@@ -34,6 +34,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "kernels.cuh"
 #include "rowvec.cuh"
@@ -48,15 +49,11 @@ constexpr int EX_THREADS2 = 384;                    // pair kernel: warps 0..3 T
 constexpr int EX_REGS_LOW = 40, EX_REGS_HIGH = 232;
 static_assert(128 * EX_REGS_LOW + 256 * EX_REGS_HIGH <= 168 * EX_THREADS2, "register split exceeds the launch allocation");
 constexpr int EX_STAGE2_BYTES = 32768;              // 128 rows x 128 bytes of A, as much of B
-// Shared memory of the pair kernel: 16-bit operands take five stages and two output buffers per epilogue warp, so
-// that a warp's next 128 bytes of columns need not wait for the last store to be read; 8-bit stages are used up
-// twice as fast and get six, with one output buffer.
-template <int KIND>
-struct ExPair {
-    static constexpr int NS = KIND == 0 ? 5 : 6;
-    static constexpr int NOUT = KIND == 0 ? 2 : 1;
-    static constexpr int OUT = EPI_WARPS * NOUT * STAGE_OUT_BYTES;
-};
+// Six stages: a pair multiplies a 16-bit stage in about 500 cycles and a load takes some 2,500 from the freed stage to
+// the filled one (by the clock, all SMs loading), so every stage counts; five stages with a second output buffer per
+// epilogue warp measured 32.6 us where six take 31.5 (20,000 rows, 24 experts of 1,024 x 479). An 8-bit stage lasts
+// half as long, and the loads bound those products: about 70 bytes per SM and clock.
+constexpr int EX_STAGES2 = 6;
 
 enum ExpertOp { EX_FWD = 0, EX_BWD = 1 };
 enum ExpertTile { ET_FWD = 0, ET_DGRAD = 1, ET_WGRAD = 2 };   // what a tile of the pair kernel computes
@@ -324,11 +321,10 @@ __device__ __forceinline__ void ex_affine(float (&v)[32], const EpiRow<NC>& er, 
 // through the warp's 4 KB stage, 128 bytes of columns at a time: whole 32-row groups by TMA (columns
 // past J are clipped), a group that holds the expert's last row by 16-byte stores of its valid rows only.
 //   row0: first output row of the warp; nvalid: its rows that exist (<= 0: none); e: expert
-//   buf: which of the warp's NOUT output buffers comes next
-template <typename TC, int NC, int OP, int KIND, int NOUT>
+template <typename TC, int NC, int OP, int KIND>
 __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>& er, int row0, int nvalid, int j0, int e,
-                                         const ExpertArgs& a, const CUtensorMap* mapC, unsigned char* stage0,
-                                         uint32_t stage_s0, int& buf) {
+                                         const ExpertArgs& a, const CUtensorMap* mapC, unsigned char* stage,
+                                         uint32_t stage_s) {
     constexpr int CW = 128 / (int)sizeof(TC);   // columns per 128 bytes: 32 (fp32) or 64
     constexpr int PER = CW / 32;                // 32-column groups per 128 bytes
     const int lane = threadIdx.x & 31;
@@ -341,11 +337,7 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>&
 #pragma unroll
             for (int p = 0; p < PER; ++p) ex_affine<NC, KIND>(acc[c * PER + p], er, c * PER + p, a);
         }
-        unsigned char* stage = stage0 + buf * STAGE_OUT_BYTES;
-        const uint32_t stage_s = stage_s0 + buf * STAGE_OUT_BYTES;
-        buf = buf + 1 == NOUT ? 0 : buf + 1;
-        // the store that last used this buffer has read it: at most NOUT - 1 are still to be read
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(NOUT - 1) : "memory");
+        if (lane == 0) bulk_wait_read0();       // the previous chunk's store has read the stage
         __syncwarp();
         unsigned char* row = stage + lane * 128;
 #pragma unroll
@@ -416,9 +408,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
     const uint32_t raw = su32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* gbase = smem_raw + (base - raw);
-    using P = ExPair<KIND>;
-    constexpr int NS = P::NS;
-    Ranges* rg = reinterpret_cast<Ranges*>(gbase + NS * EX_STAGE2_BYTES + P::OUT);
+    constexpr int NS = EX_STAGES2;
+    Ranges* rg = reinterpret_cast<Ranges*>(gbase + NS * EX_STAGE2_BYTES + OUT_BYTES);
     ExBars<NS>* bars = reinterpret_cast<ExBars<NS>*>(rg + 1);
     const int warp = uni(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -566,9 +557,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EX_REGS_HIGH));
         const int ew = warp - 4, q = warp & 3, h = ew >> 2;
-        unsigned char* stage = gbase + NS * EX_STAGE2_BYTES + ew * P::NOUT * STAGE_OUT_BYTES;
-        const uint32_t stage_s = base + NS * EX_STAGE2_BYTES + ew * P::NOUT * STAGE_OUT_BYTES;
-        int buf = 0;
+        unsigned char* stage = gbase + NS * EX_STAGE2_BYTES + ew * STAGE_OUT_BYTES;
+        const uint32_t stage_s = base + NS * EX_STAGE2_BYTES + ew * STAGE_OUT_BYTES;
         const uint32_t lead_tempty0 = map_rank(su32(&bars->tempty[0]), 0);
         const uint32_t lead_tempty1 = map_rank(su32(&bars->tempty[1]), 0);
         uint32_t part = 0;
@@ -600,11 +590,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
             }
             if (timed_out) break;
             if constexpr (OP == EX_FWD) {
-                ex_store<TC, 4, ET_FWD, KIND, P::NOUT>(acc, er, row0, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
+                ex_store<TC, 4, ET_FWD, KIND>(acc, er, row0, nvalid, j0, e, a, &maps.c, stage, stage_s);
             } else if (dw) {
-                ex_store<TW, 4, ET_WGRAD, KIND, P::NOUT>(acc, er, row0, nvalid, j0, e, a, &maps.wc, stage, stage_s, buf);
+                ex_store<TW, 4, ET_WGRAD, KIND>(acc, er, row0, nvalid, j0, e, a, &maps.wc, stage, stage_s);
             } else {
-                ex_store<TC, 4, ET_DGRAD, KIND, P::NOUT>(acc, er, row0, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
+                ex_store<TC, 4, ET_DGRAD, KIND>(acc, er, row0, nvalid, j0, e, a, &maps.c, stage, stage_s);
             }
         }
         if (timed_out) *abort = 1;
@@ -759,7 +749,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t stage_s = base + NS * T::STAGE + ew * STAGE_OUT_BYTES;
         const int parts = (nk + PART - 1) / PART;
         uint32_t part = 0;
-        int buf = 0;
         for (long long t = blockIdx.x; !timed_out && walk.seek(t, mb, cb); t += gridDim.x) {
             const int e = walk.e, row = rg->begin[e] + mb * 128 + q * 32;
             const bool some = active && row < rg->end[e];
@@ -784,7 +773,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(&bars->tempty[b]);
             }
             if (timed_out) break;
-            if (some) ex_store<TC, NC, ET_FWD, KIND, 1>(acc, er, row, nvalid, j0, e, a, &maps.c, stage, stage_s, buf);
+            if (some) ex_store<TC, NC, ET_FWD, KIND>(acc, er, row, nvalid, j0, e, a, &maps.c, stage, stage_s);
         }
         if (timed_out) *abort = 1;
         if (lane == 0) bulk_wait_all0();
@@ -798,10 +787,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-template <int KIND>
-constexpr int EX_SMEM2 = ExPair<KIND>::NS * EX_STAGE2_BYTES + ExPair<KIND>::OUT + (int)sizeof(Ranges) +
-                         (int)sizeof(ExBars<ExPair<KIND>::NS>) + 256;
-static_assert(EX_SMEM2<EX_F16> <= 227 * 1024 && EX_SMEM2<EX_F8> <= 227 * 1024, "shared memory");
+constexpr int EX_SMEM2 =
+    EX_STAGES2 * EX_STAGE2_BYTES + OUT_BYTES + (int)sizeof(Ranges) + (int)sizeof(ExBars<EX_STAGES2>) + 256;
+static_assert(EX_SMEM2 <= 227 * 1024, "shared memory");
 static_assert(ExTile<64>::SMEM <= 227 * 1024 && ExTile<128>::SMEM <= 227 * 1024, "shared memory");
 
 // ------------------------------------------------------------------ backward: dP, bias sums, padded last blocks
@@ -1028,10 +1016,10 @@ template <typename TC, typename TW, int OP, int KIND>
 dlrm_status launch_pair(const typename PairMaps<OP>::t& maps, const ExpertArgs& a, uint32_t id, uint32_t id_dw,
                         long long tiles, cudaStream_t st) {
     auto kern = expert_pair_kernel<TC, TW, OP, KIND>;
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, EX_SMEM2<KIND>);
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, EX_SMEM2);
     const int pairs = device_sms() / 2;
     const dim3 grid((unsigned)(2 * std::min<long long>(tiles, pairs)));
-    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(EX_THREADS2), (size_t)EX_SMEM2<KIND>, st, maps, a, id, id_dw));
+    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(EX_THREADS2), (size_t)EX_SMEM2, st, maps, a, id, id_dw));
     return DLRM_OK;
 }
 
@@ -1057,13 +1045,23 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
     using namespace tc;
     const int es = ex_size(dt), ke = 128 / es;
     const ExpertArgs a{E, M, N, 0, K, true, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, err};
-    // SM pairs once their 256 x 256 tiles can fill them (rows spread evenly over the experts). Otherwise one SM per
-    // tile: 64 columns wide if that gives every tile an SM of its own, else 128 (12 rows of 8 experts, 4,096 x 1,024
-    // bf16: 13.6 us at 128, 15.5 at 64, 17.6 at 32; a k-block's issue costs 420 to 465 cycles at any width).
-    const long long nb2 = (N + 255) / 256, sms = device_sms();
-    const bool pair = ((long long)M / 256) * nb2 >= sms / 2;
-    const long long rb = std::max<long long>((M + 127) / 128, std::min(E, M));
-    const bool narrow = rb * ((N + 63) / 64) <= sms;
+    // Tiles of 256 x 256 on SM pairs, or of 128 x 128 or 128 x 64 on single SMs: whichever rounds of tiles take least,
+    // by times measured on both sides (us: a round's k-blocks and what it costs besides; the pairs' later start).
+    // bf16, 4 experts of 4,096 x 1,024, 8,192 rows: pairs 56, single SMs 70; 512 rows: 12.9 and 12.5; 4 experts of
+    // 1,024 x 4,096, 4,096 rows: 29 and 37, 2,048 rows: 26 and 21. 12 rows of 8 experts of 4,096 x 1,024: 13.6 at 128
+    // columns, 15.5 at 64 (and 17.6 at 32: a k-block's issue costs 420 to 465 cycles at any width).
+    const long long sms = device_sms(), used = std::min(E, M);
+    const double nk = (K + ke - 1) / ke;
+    auto rounds = [&](long long rows_per, long long cols, long long units) {
+        // row blocks of unevenly filled experts: half a block each is lost to their last rows, and where most fit one
+        // block some need two
+        const double full = (double)M / rows_per;
+        const double rb = full >= used ? full + 0.5 * used : used + 0.4 * full;
+        return std::ceil(rb * (double)((N + cols - 1) / cols) / (double)units);
+    };
+    const double t256 = rounds(256, 256, sms / 2) * (0.3 * nk + 1.5) + 2.5;
+    const double t128 = rounds(128, 128, sms) * (0.245 * nk + 1.0), t64 = rounds(128, 64, sms) * (0.22 * nk + 1.0);
+    const bool pair = t256 < std::min(t128, t64), narrow = t64 < t128;
     ExpertMaps maps{};
     // the tile kernel's A comes in boxes of 128 rows or, for row blocks of at most 32, of 32
     const bool only32 = !pair && M <= 32;
@@ -1075,7 +1073,7 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
     const int fmt = dt == DLRM_BF16 ? 1 : 0;
 #define DLRM_EX_FWD(TC, KIND)                                                                     \
     return pair ? launch_pair<TC, TC, EX_FWD, KIND>(maps, a, ex_idesc(fmt, false, false, 256, 256), \
-                                                    0u, most_tiles(E, M, 256, nb2), st)           \
+                                                    0u, most_tiles(E, M, 256, (N + 255) / 256), st) \
            : narrow ? launch_tile<TC, KIND, 64>(maps, a, fmt, st)                                 \
                     : launch_tile<TC, KIND, 128>(maps, a, fmt, st);
     if (dt == DLRM_E4M3) {

@@ -109,7 +109,7 @@ dlrm_status lookup_vec(const LookupArgs& a, cudaStream_t st) {
 
 template <typename TI, typename TO>
 dlrm_status lookup_to(const LookupArgs& a, cudaStream_t st) {
-    // runs of 16 bytes of the narrower type where every row allows it, else of 4 bytes, else single elements
+    // runs of 16 bytes of the narrower type where every row allows it, else the widest that do
     constexpr int W = 16 / (int)(sizeof(TI) < sizeof(TO) ? sizeof(TI) : sizeof(TO));
     auto fits = [&](int vec) {
         const int bi = std::min(16, vec * (int)sizeof(TI)), bo = std::min(16, vec * (int)sizeof(TO));
@@ -117,6 +117,8 @@ dlrm_status lookup_to(const LookupArgs& a, cudaStream_t st) {
                rows_on(a.out, a.ldo * (long long)sizeof(TO), bo);
     };
     if (fits(W)) return lookup_vec<TI, TO, W>(a, st);
+    if constexpr (W > 4)
+        if (fits(4)) return lookup_vec<TI, TO, 4>(a, st);
     if (fits(2)) return lookup_vec<TI, TO, 2>(a, st);
     return lookup_vec<TI, TO, 1>(a, st);
 }
@@ -673,6 +675,8 @@ dlrm_status sum_to(const SumArgs& a, cudaStream_t st) {
                rows_on(a.dT, (long long)a.d * sizeof(TO), bo);
     };
     if (fits(W)) return sum_vec<TI, TO, W>(a, st);
+    if constexpr (W > 4)
+        if (fits(4)) return sum_vec<TI, TO, 4>(a, st);
     if (fits(2)) return sum_vec<TI, TO, 2>(a, st);
     return sum_vec<TI, TO, 1>(a, st);
 }

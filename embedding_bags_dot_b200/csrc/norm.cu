@@ -467,6 +467,8 @@ dlrm_status fwd_t(const NormFwdArgs& a, bool q8, cudaStream_t st) {
     int vec = u.vec();
     while (a.d % vec) vec >>= 1;
     if (vec == W) return q8 ? fwd_vec<T, W, true>(a, st) : fwd_vec<T, W, false>(a, st);
+    if constexpr (W > 4)
+        if (vec == 4) return q8 ? fwd_vec<T, 4, true>(a, st) : fwd_vec<T, 4, false>(a, st);
     if (vec >= 2) return q8 ? fwd_vec<T, 2, true>(a, st) : fwd_vec<T, 2, false>(a, st);
     return q8 ? fwd_vec<T, 1, true>(a, st) : fwd_vec<T, 1, false>(a, st);
 }
@@ -509,6 +511,8 @@ dlrm_status bwd_t(const NormBwdArgs& a, int& nblocks, cudaStream_t st) {
     int vec = u.vec();
     while (a.d % vec) vec >>= 1;
     if (vec == W) return bwd_vec<T, W>(a, nblocks, st);
+    if constexpr (W > 4)
+        if (vec == 4) return bwd_vec<T, 4>(a, nblocks, st);
     if (vec >= 2) return bwd_vec<T, 2>(a, nblocks, st);
     return bwd_vec<T, 1>(a, nblocks, st);
 }
