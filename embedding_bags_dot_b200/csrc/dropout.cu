@@ -8,10 +8,11 @@
 // kept when its word is at least p * 2^32 (rounded to an integer), so the
 // probability is right to 2^-33.
 //
-// Bound by memory at the larger sizes (2 or 3 arrays read and written once)
-// and by the integer pipe close behind it: ten rounds of two 32 x 32 -> 64
-// products serve four elements. Each thread takes runs of 16 bytes (four or
-// eight elements, one or two generator calls). seed and offset are read from
+// Bound by memory with fp32 elements or a residual (33.5 M bf16 with residual:
+// 34 us, 5.9 TB/s), by the integer pipe without (31 us, 4.4 TB/s): ten rounds
+// of two 32 x 32 -> 64 products serve four elements. Each thread takes two runs
+// of 16 bytes at a time (four or eight elements, one or two generator calls
+// each). seed and offset are read from
 // device memory so that a captured graph draws anew when they are changed
 // between replays.
 #include "kernels.cuh"
@@ -57,9 +58,10 @@ struct DropArgs {
     float scale;
 };
 
-// VEC = elements per 16 bytes, or 4 with element-wise accesses (ALIGNED = false).
-template <typename T, bool RES, bool ALIGNED>
-__global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ DropArgs a) {
+// VEC = elements per 16 bytes, or 4 with element-wise accesses (ALIGNED = false). SMALL: the counter's low half
+// fits 32 bits, so that two of the twenty products are the same for all elements and leave the loop.
+template <typename T, bool RES, bool ALIGNED, bool SMALL>
+__global__ void __launch_bounds__(256, 5) dropout_kernel(const __grid_constant__ DropArgs a) {
     pdl_wait();
     constexpr int VEC = ALIGNED ? 16 / (int)sizeof(T) : 4;
     const T* x = static_cast<const T*>(a.x);
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ Dr
             float v[VEC];
 #pragma unroll
             for (int g = 0; g < VEC / 4; ++g) {
-                const uint4 w = philox4x32_10((unsigned long long)(i / 4 + g), c2, c3, keys);
+                const uint4 w = philox4x32_10(SMALL ? (unsigned long long)(uint32_t)(i / 4 + g) : (unsigned long long)(i / 4 + g), c2, c3, keys);
                 const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -121,9 +123,15 @@ dlrm_status launch_t(const DropArgs& a, cudaStream_t st) {
     const bool al = rows_on(a.x, 0, 16) && rows_on(a.y, 0, 16) && rows_on(a.residual, 0, 16);
     const int vec = al ? 16 / (int)sizeof(T) : 4;
     const long long want = (a.n + 512ll * vec - 1) / (512ll * vec);
-    const long long most = 8ll * device_sms();
+    // many short blocks: one wave of 8 an SM measured 38.7 us where 40 take 34.3 (33.5 M bf16 with residual)
+    const long long most = 40ll * device_sms();
     const dim3 grid((unsigned)(want < most ? want : most));
-#define DLRM_DROP(RES, AL) DLRM_PDL_CHECK(launch_pdl(dropout_kernel<T, RES, AL>, grid, dim3(256), 0, st, a))
+    const bool small = a.n <= 4ll << 32;
+#define DLRM_DROP(RES, AL)                                                                          \
+    do {                                                                                            \
+        if (small) DLRM_PDL_CHECK(launch_pdl(dropout_kernel<T, RES, AL, true>, grid, dim3(256), 0, st, a)); \
+        else DLRM_PDL_CHECK(launch_pdl(dropout_kernel<T, RES, AL, false>, grid, dim3(256), 0, st, a));      \
+    } while (0)
     if (a.residual) {
         if (al) DLRM_DROP(true, true);
         else DLRM_DROP(true, false);

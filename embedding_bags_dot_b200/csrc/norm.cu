@@ -444,7 +444,10 @@ dlrm_status fwd_vec(const NormFwdArgs& a, cudaStream_t st) {
     // few rows: the latency of a row counts, so it is spread over as many threads as it has runs
     if (a.rows <= sms && one <= 1024)
         return norm_launch(rmsnorm_fwd_kernel<T, VEC, NV, true, Q8, 1024, false>, (unsigned)a.rows, one, 0, a, st);
-    const int two = norm_threads(a.d, 2 * W);
+    // two runs a thread where the runs are whole, else eight elements in smaller pieces (16 of them a thread took
+    // 70 us where 8 take 45: 16,384 odd-width bf16 rows)
+    constexpr int PT = VEC == W ? 2 * W : 8;
+    const int two = norm_threads(a.d, PT);
     if (two > 1024) {
         const int t = norm_threads(a.d, 32);
         return norm_launch(rmsnorm_fwd_kernel<T, VEC, 32 / VEC, true, Q8, 1024, false>,
@@ -452,8 +455,8 @@ dlrm_status fwd_vec(const NormFwdArgs& a, cudaStream_t st) {
     }
     const unsigned grid = (unsigned)std::min<long long>(a.rows, sms * (1024 / two));
     const size_t smem = VEC == W ? (size_t)FWD_RING * 2 * 2 * 16 * two : 0;
-    if (two > 256) return norm_launch(rmsnorm_fwd_kernel<T, VEC, 2 * NV, true, Q8, 1024, VEC == W>, grid, two, smem, a, st);
-    return norm_launch(rmsnorm_fwd_kernel<T, VEC, 2 * NV, true, Q8, 256, VEC == W>, grid, two, smem, a, st);
+    if (two > 256) return norm_launch(rmsnorm_fwd_kernel<T, VEC, PT / VEC, true, Q8, 1024, VEC == W>, grid, two, smem, a, st);
+    return norm_launch(rmsnorm_fwd_kernel<T, VEC, PT / VEC, true, Q8, 256, VEC == W>, grid, two, smem, a, st);
 }
 
 template <typename T>
@@ -490,14 +493,15 @@ dlrm_status bwd_vec(const NormBwdArgs& a, int& nblocks, cudaStream_t st) {
         const size_t smem = a.partial ? sizeof(float) * 4 * W * 32 : 0;
         return norm_launch(rmsnorm_bwd_kernel<T, VEC, NV, false, 128, false>, nblocks, 128, smem, a, st);
     }
-    const int two = norm_threads(a.d, 2 * W), wide = norm_threads(a.d, 32);
+    constexpr int PT = VEC == W ? 2 * W : 8;
+    const int two = norm_threads(a.d, PT), wide = norm_threads(a.d, 32);
     nblocks = (int)std::min<long long>(a.rows, std::min(bwd_resident(two > 1024 ? wide : two), bwd_most(a.d)));
     if (two > 1024)
         return norm_launch(rmsnorm_bwd_kernel<T, VEC, 32 / VEC, true, 1024, false>, nblocks, wide, 0, a, st);
     const size_t smem = VEC == W ? (size_t)BWD_RING * 3 * 2 * 16 * two : 0;
     if (two > 256)
-        return norm_launch(rmsnorm_bwd_kernel<T, VEC, 2 * NV, true, 1024, VEC == W>, nblocks, two, smem, a, st);
-    return norm_launch(rmsnorm_bwd_kernel<T, VEC, 2 * NV, true, 256, VEC == W>, nblocks, two, smem, a, st);
+        return norm_launch(rmsnorm_bwd_kernel<T, VEC, PT / VEC, true, 1024, VEC == W>, nblocks, two, smem, a, st);
+    return norm_launch(rmsnorm_bwd_kernel<T, VEC, PT / VEC, true, 256, VEC == W>, nblocks, two, smem, a, st);
 }
 
 template <typename T>
