@@ -579,16 +579,22 @@ def _same_device(where: str, *tensors) -> int:
     return dev
 
 
+# the two lookups of every call, by torch's own short cuts where it has them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(where: str, dev: int, stream, *args):
     """Runs the C entry point `where` on the tensors' device, which need not be the current one."""
     fn = getattr(_lib or lib(), where)
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = _raw_stream(dev)
     elif isinstance(stream, torch.cuda.Stream):
         if stream.device.index != dev:
             _refuse(where)
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):

@@ -24,6 +24,9 @@ bool tight(const void* p, int64_t ld, int64_t width, int dt) {
     return p && on(p, 16) && ld >= width && ld < INT31 && (ld * (int64_t)elem(dt)) % 16 == 0;
 }
 
+// One expert's weights span less than a tensor map's largest stride.
+bool spans(int N, int64_t ld, int dt) { return (int64_t)N * ld * (int64_t)elem(dt) < (int64_t)1 << 40; }
+
 dlrm_status experts_sizes(int E, int M, int N, int K) {
     if (E < 1 || M < 0 || N < 1 || K < 1) return DLRM_ERR_INVALID_ARG;
     if (E > DLRM_MAX_EXPERTS) return DLRM_ERR_UNSUPPORTED;
@@ -133,6 +136,7 @@ dlrm_status dlrm_experts_fwd(int E, int M, int N, int K, const int32_t* offsets,
     if (!offsets || !on(offsets, 4) || !tight(X, ldx, K, dt) || !tight(W, ldw, K, dt) || !tight(Y, ldy, N, y_dt) ||
         !on(bias, 4))
         return DLRM_ERR_INVALID_ARG;
+    if (!spans(N, ldw, dt)) return DLRM_ERR_UNSUPPORTED;
     const bool scaled = dt == DLRM_E4M3;
     if (scaled != (x_scale != nullptr) || scaled != (w_scale != nullptr) || !on(x_scale, 4) || !on(w_scale, 4))
         return DLRM_ERR_INVALID_ARG;
@@ -163,6 +167,7 @@ dlrm_status dlrm_experts_bwd(int E, int M, int N, int K, const int32_t* offsets,
     if (M > 0 && (!tight(dY, lddy, N, dt) || (relu && !tight(Y, ldy, N, dt)) || (dW && !tight(X, ldx, K, dt)) ||
                   (dX && !tight(W, ldw, K, dt))))
         return DLRM_ERR_INVALID_ARG;
+    if ((dX && M > 0 && !spans(N, ldw, dt)) || (dW && !spans(N, lddw, dw_dt))) return DLRM_ERR_UNSUPPORTED;
     if (!experts_supported()) return DLRM_ERR_UNSUPPORTED;
     return launch_experts_bwd(E, M, N, K, offsets, dY, lddy, relu ? Y : nullptr, ldy, X, ldx, W, ldw, dt, dX, lddx, dx_dt,
                               dW, lddw, dw_dt, db, static_cast<char*>(ws), cs(stream));

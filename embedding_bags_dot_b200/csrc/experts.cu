@@ -1117,6 +1117,30 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
     float* part = reinterpret_cast<float*>(ws + L.part);
     const void* dP = relu ? (const void*)(ws + L.dp) : dY;
     const long long ldp = relu ? L.ldp : lddy;
+    // every map is encoded before anything is launched
+    GradMaps maps{};
+    const long long nbk = (K + 255) / 256;
+    long long tiles = 0;
+    a.rows_out = dX && M > 0;
+    if (a.rows_out) {
+        if (!ex_map(&maps.a, dP, 2, dt, 2, N, M, 1, ldp, 64, 128) || !ex_map(&maps.b, W, 2, dt, 3, K, N, E, ldw, 64, 64) ||
+            !ex_map(&maps.c, dX, ex_size(dx_dt), dx_dt, 2, K, M, 1, lddx, 128 / ex_size(dx_dt), 32))
+            return DLRM_ERR_CUDA;
+        tiles += most_tiles(E, M, 256, nbk);
+    }
+    if (dW) {
+        // without rows nothing is loaded; the maps still need an address
+        const void* pa = M > 0 ? dP : ws + L.tail_dp;
+        const void* pb = M > 0 ? X : ws + L.tail_x;
+        const long long rows = M > 0 ? M : 1;
+        if (!ex_map(&maps.wa, pa, 2, dt, 2, N, rows, 1, M > 0 ? ldp : L.ldp, 64, 64) ||
+            !ex_map(&maps.wb, pb, 2, dt, 2, K, rows, 1, M > 0 ? ldx : L.ldtx, 64, 64) ||
+            !ex_map(&maps.at, ws + L.tail_dp, 2, dt, 3, N, PREP_ROWS, E, L.ldp, 64, 64) ||
+            !ex_map(&maps.bt, ws + L.tail_x, 2, dt, 3, K, PREP_ROWS, E, L.ldtx, 64, 64) ||
+            !ex_map(&maps.wc, dW, ex_size(dw_dt), dw_dt, 3, K, N, E, lddw, 128 / ex_size(dw_dt), 32))
+            return DLRM_ERR_CUDA;
+        tiles += (long long)E * ((N + 255) / 256) * nbk;
+    }
     if (M > 0 && (relu || db || dW)) {
         PrepArgs p{};
         p.x = a;
@@ -1148,30 +1172,7 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
                                   (const float*)part, db));
         a.count = false;
     }
-    if ((!dX || M == 0) && !dW) return DLRM_OK;
-    GradMaps maps{};
-    const long long nbk = (K + 255) / 256;
-    long long tiles = 0;
-    a.rows_out = dX && M > 0;
-    if (a.rows_out) {
-        if (!ex_map(&maps.a, dP, 2, dt, 2, N, M, 1, ldp, 64, 128) || !ex_map(&maps.b, W, 2, dt, 3, K, N, E, ldw, 64, 64) ||
-            !ex_map(&maps.c, dX, ex_size(dx_dt), dx_dt, 2, K, M, 1, lddx, 128 / ex_size(dx_dt), 32))
-            return DLRM_ERR_CUDA;
-        tiles += most_tiles(E, M, 256, nbk);
-    }
-    if (dW) {
-        // without rows nothing is loaded; the maps still need an address
-        const void* pa = M > 0 ? dP : ws + L.tail_dp;
-        const void* pb = M > 0 ? X : ws + L.tail_x;
-        const long long rows = M > 0 ? M : 1;
-        if (!ex_map(&maps.wa, pa, 2, dt, 2, N, rows, 1, M > 0 ? ldp : L.ldp, 64, 64) ||
-            !ex_map(&maps.wb, pb, 2, dt, 2, K, rows, 1, M > 0 ? ldx : L.ldtx, 64, 64) ||
-            !ex_map(&maps.at, ws + L.tail_dp, 2, dt, 3, N, PREP_ROWS, E, L.ldp, 64, 64) ||
-            !ex_map(&maps.bt, ws + L.tail_x, 2, dt, 3, K, PREP_ROWS, E, L.ldtx, 64, 64) ||
-            !ex_map(&maps.wc, dW, ex_size(dw_dt), dw_dt, 3, K, N, E, lddw, 128 / ex_size(dw_dt), 32))
-            return DLRM_ERR_CUDA;
-        tiles += (long long)E * ((N + 255) / 256) * nbk;
-    }
+    if (tiles == 0) return DLRM_OK;
     const int fmt = dt == DLRM_BF16 ? 1 : 0;
     const uint32_t id = ex_idesc(fmt, false, true, 256, 256), id_dw = ex_idesc(fmt, true, true, 256, 256);
     // an output that is not asked for takes the other's type

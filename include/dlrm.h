@@ -424,6 +424,8 @@ dlrm_status dlrm_embbag_sgd(const dlrm_tables* T, int B, const int32_t* offsets,
  *    a multiple of the element size (rows on 16-byte boundaries are fastest).
  *  - Sums and statistics are fp32; each output is rounded to its type once.
  *    Results do not depend on timing: the same call gives the same bits.
+ *  - Outputs must not overlap inputs, or one another, except where a call says
+ *    so.
  *  - Sizes of zero (n, rows, M) are valid and launch what the outputs still
  *    need (zero gradients), or nothing.
  *  - Calls that share a workspace, or that write the same outputs, must follow

@@ -29,11 +29,12 @@ def within(got, want, bound, what):
         f"{what}: {int((over > 0).sum())} of {over.numel()} beyond the bound, worst by {float(over.max()):.3g}"
 
 
-def philox(n, seed, offset):
-    """Words 0 .. n - 1 of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011): counter {i / 4, offset}, key seed."""
+def philox(n, seed, offset, first=0):
+    """Words first .. first + n - 1 (first a multiple of 4) of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011):
+    counter {i / 4, offset}, key seed."""
     g = (n + 3) // 4
     mask, sh = np.uint64(0xFFFFFFFF), np.uint64(32)
-    i = np.arange(g, dtype=np.uint64)
+    i = np.arange(g, dtype=np.uint64) + np.uint64(first // 4)
     c = [i & mask, i >> sh, np.full(g, offset & 0xFFFFFFFF, np.uint64), np.full(g, (offset >> 32) & 0xFFFFFFFF, np.uint64)]
     k0, k1 = seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF
     for _ in range(10):

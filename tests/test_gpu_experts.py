@@ -225,6 +225,23 @@ def test_gradients_keep_other_rows_out(relu):
         assert torch.equal(a, b)
 
 
+def test_rows_before_the_first_expert():
+    sizes, N, K = [70, 0, 200], 48, 64
+    g = torch.Generator().manual_seed(12)
+    M = 5 + sum(sizes) + 9
+    X, W = _values("int", (M, K), g).bfloat16(), _values("int", (3, N, K), g).bfloat16()
+    offs = _offsets(sizes, first=5)
+    Y, st = _forward(X, W, offs, torch.float32)
+    assert st[0] == E.OK
+    _check_forward(Y, X, W, offs, None, False, torch.float32, exact=True)
+    dY = _values("int", (M, N), g).bfloat16()
+    (dX, dW, db), st = _backward(dY, X, W, offs, None, torch.bfloat16, torch.float32)
+    (wX, wW, wb), _ = R.experts_grad(dY, X, W, offs, None)
+    assert st[0] == E.OK and torch.equal(dW.cpu().double(), wW) and torch.equal(db.cpu().double(), wb)
+    assert torch.equal(dX.cpu()[5:275].double(), wX[5:275].to(torch.bfloat16).double())
+    assert bool((dX.cpu()[:5] == -7).all()) and bool((dX.cpu()[275:] == -7).all())
+
+
 def test_no_rows_at_all():
     X, W = torch.zeros((0, 64), dtype=torch.bfloat16), torch.ones((3, 40, 64), dtype=torch.bfloat16)
     offs = torch.zeros(4, dtype=torch.int32)
