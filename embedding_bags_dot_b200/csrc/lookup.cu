@@ -10,8 +10,8 @@
 // once; no atomics on values, so the result does not depend on timing.
 //   1. (id, position) pairs are sorted by id, stably: an LSD radix sort whose
 //      digits are as wide as the table needs (two passes up to 2^20 rows), in
-//      one block's shared memory up to 4,096 pairs, else a histogram and a
-//      scatter per pass over blocks of 2,048.
+//      one block up to 2,048 pairs, a cluster of eight up to 16,384, else with a
+//      histogram and a scatter launch per pass over blocks of 2,048.
 //      The sort takes few SMs and little bandwidth, so the other blocks of
 //      its launches write the table's zeros meanwhile; rows with lookups are
 //      written again by the next steps.
@@ -26,6 +26,7 @@
 
 #include "kernels.cuh"
 #include "rowvec.cuh"
+#include "tcgen05.cuh"
 
 namespace dlrm {
 namespace {
@@ -137,10 +138,11 @@ constexpr int RS_ITEMS = 8;            // keys per thread and tile
 // Ranking a warp's 32 keys costs about a hundred instructions, so a pass takes an SM the longer the more of them it
 // has: 8,192 pairs on one SM took 10 us a pass. Blocks are small, and short calls alone stay in one.
 constexpr int RS_THREADS = 256;
+constexpr int RS_WARPS = RS_THREADS / 32;
 constexpr int RS_TILE = RS_THREADS * RS_ITEMS;
 constexpr int RS_BLOCKS_MAX = 296;
-constexpr int SORT1_THREADS = 512;     // the one-block sort takes up to 4,096 pairs
-constexpr int SORT1_MAX = SORT1_THREADS * RS_ITEMS;
+constexpr int SORT1_MAX = RS_TILE;      // pairs the one-block sort takes
+constexpr int SORT8_MAX = 8 * RS_TILE;  // pairs the eight-block cluster's sort takes
 
 // A share of the table's bytes, zeroed by the blocks of a sorting launch that do not sort.
 struct Zeros {
@@ -176,26 +178,24 @@ __device__ __forceinline__ uint32_t pass_key(const void* in, long long i, long l
     }
 }
 
-// Shared memory of a sorting block of W warps.
+// Shared memory of a sorting block (RS_WARPS warps).
 struct SortMem {
-    unsigned short* wc;     // [W][radix]: keys of a digit in each warp, then their places by warp
+    unsigned short* wc;     // [RS_WARPS][radix]: keys of a digit in each warp, then their places by warp
     int* tot;               // [radix]
     int* wsum;              // [32]
     uint32_t* keys;         // [tile]: the tile's pairs in order
     uint32_t* vals;
 };
-__device__ __forceinline__ SortMem sort_mem(unsigned char* p, int warps, int radix) {
+__device__ __forceinline__ SortMem sort_mem(unsigned char* p, int radix) {
     SortMem s;
     s.wc = reinterpret_cast<unsigned short*>(p);
-    s.tot = reinterpret_cast<int*>(p + 2 * warps * radix);
+    s.tot = reinterpret_cast<int*>(p + 2 * RS_WARPS * radix);
     s.wsum = s.tot + radix;
     s.keys = reinterpret_cast<uint32_t*>(s.wsum + 32);
-    s.vals = s.keys + warps * 32 * RS_ITEMS;
+    s.vals = s.keys + RS_TILE;
     return s;
 }
-size_t sort_bytes(int warps, int radix) {
-    return 2 * (size_t)warps * radix + 4 * (size_t)radix + 128 + 8 * (size_t)warps * 32 * RS_ITEMS;
-}
+constexpr size_t sort_bytes(int radix) { return 2 * (size_t)RS_WARPS * radix + 4 * (size_t)radix + 128 + 8 * (size_t)RS_TILE; }
 
 // place[e] = how many keys of the block with the same digit come before the thread's e-th; sm.tot[digit] = how many
 // there are. Key e of lane l in warp w is number w * 256 + e * 32 + l of the tile; those from `cnt` on do not count.
@@ -203,9 +203,9 @@ size_t sort_bytes(int warps, int radix) {
 // are summed over the warps.
 __device__ __forceinline__ void rank_keys(const uint32_t (&key)[RS_ITEMS], int cnt, int shift, int radix, const SortMem& sm,
                                           int (&place)[RS_ITEMS]) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = warp * (32 * RS_ITEMS) + lane;
-    for (int i = threadIdx.x; i < warps * radix / 8; i += blockDim.x)
+    for (int i = threadIdx.x; i < RS_WARPS * radix / 8; i += RS_THREADS)
         reinterpret_cast<uint4*>(sm.wc)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     unsigned short* mine = sm.wc + warp * radix;
@@ -223,15 +223,19 @@ __device__ __forceinline__ void rank_keys(const uint32_t (&key)[RS_ITEMS], int c
         __syncwarp();
     }
     __syncthreads();
-    for (int dg = threadIdx.x; dg < radix; dg += blockDim.x) {
-        int run = 0;
-#pragma unroll 8
-        for (int w = 0; w < warps; ++w) {
-            const int c = sm.wc[w * radix + dg];
-            sm.wc[w * radix + dg] = (unsigned short)run;
-            run += c;
+    // two neighbouring digits a thread (one word of counts per warp), all warps' words loaded before any is written
+    for (int d2 = threadIdx.x; d2 < radix / 2; d2 += RS_THREADS) {
+        uint32_t* col = reinterpret_cast<uint32_t*>(sm.wc) + d2;
+        uint32_t c[RS_WARPS], run = 0;
+#pragma unroll
+        for (int w = 0; w < RS_WARPS; ++w) c[w] = col[w * (radix / 2)];
+#pragma unroll
+        for (int w = 0; w < RS_WARPS; ++w) {
+            col[w * (radix / 2)] = run;
+            run += c[w];          // both halves at once: a tile's counts stay below 2^16
         }
-        sm.tot[dg] = run;
+        sm.tot[2 * d2] = (int)(run & 0xffffu);
+        sm.tot[2 * d2 + 1] = (int)(run >> 16);
     }
     __syncthreads();
 #pragma unroll
@@ -271,7 +275,7 @@ __device__ __forceinline__ void scan_digits(int* x, int radix, int* wsum) {
 
 // The whole sort in one block, the pairs going round through shared memory. Indices outside the table get id m
 // and end up last.
-__global__ void __launch_bounds__(SORT1_THREADS) sort_one_block_kernel(int n, long long m, int passes, int bits,
+__global__ void __launch_bounds__(RS_THREADS) sort_one_block_kernel(int n, long long m, int passes, int bits,
                                                                     const int32_t* __restrict__ idx,
                                                                     uint32_t* __restrict__ keys,
                                                                     uint32_t* __restrict__ vals, ErrRecord* err,
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(SORT1_THREADS) sort_one_block_kernel(int n, lo
         return;
     }
     const int radix = 1 << bits;
-    const SortMem sm = sort_mem(sort_smem, blockDim.x >> 5, radix);
+    const SortMem sm = sort_mem(sort_smem, radix);
     const int first = (threadIdx.x >> 5) * (32 * RS_ITEMS) + (threadIdx.x & 31);
     uint32_t key[RS_ITEMS], val[RS_ITEMS];
     unsigned bad = 0;
@@ -322,6 +326,77 @@ __global__ void __launch_bounds__(SORT1_THREADS) sort_one_block_kernel(int n, lo
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         keys[i] = sm.keys[i];
         vals[i] = sm.vals[i];
+    }
+}
+
+// The whole sort in one cluster of eight blocks, 2,048 pairs each: the blocks read one another's digit counts from
+// shared memory, and a cluster barrier stands between passes instead of two launches. The result is in buffer
+// (passes - 1) & 1. The other clusters of the launch write zeros.
+__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(RS_THREADS)
+    sort_cluster_kernel(int n, long long m, int passes, int bits, const int32_t* __restrict__ idx, uint32_t* keys0,
+                        uint32_t* vals0, uint32_t* keys1, uint32_t* vals1, ErrRecord* err,
+                        const __grid_constant__ Zeros zeros) {
+    pdl_wait();
+    extern __shared__ __align__(16) unsigned char sort_smem[];
+    __shared__ int next[1 << DIG_BITS_MAX], earlier[1 << DIG_BITS_MAX];
+    if (blockIdx.x >= 8) {
+        write_zeros(zeros);
+        return;
+    }
+    const int radix = 1 << bits;
+    const SortMem sm = sort_mem(sort_smem, radix);
+    const int rank = (int)tc::cluster_rank(), t0 = rank * RS_TILE;
+    const int cnt = n - t0 < 0 ? 0 : n - t0 < RS_TILE ? n - t0 : RS_TILE;
+    const int first = (threadIdx.x >> 5) * (32 * RS_ITEMS) + (threadIdx.x & 31);
+    const uint32_t tot_s = tc::su32(sm.tot);
+    unsigned bad = 0;
+    for (int p = 0; p < passes; ++p) {
+        const uint32_t *kin = p & 1 ? keys0 : keys1, *vin = p & 1 ? vals0 : vals1;
+        uint32_t *ko = p & 1 ? keys1 : keys0, *vo = p & 1 ? vals1 : vals0;
+        uint32_t key[RS_ITEMS], val[RS_ITEMS];
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e) {
+            const int i = first + e * 32;
+            key[e] = val[e] = 0;
+            if (i < cnt) {
+                if (p == 0) {
+                    key[e] = pass_key<true>(idx, t0 + i, m);
+                    val[e] = (uint32_t)(t0 + i);
+                    bad += key[e] == (uint32_t)m;
+                } else {
+                    // written by the cluster's other blocks: from L2
+                    key[e] = __ldcg(kin + t0 + i);
+                    val[e] = __ldcg(vin + t0 + i);
+                }
+            }
+        }
+        if (p == 0) report_warp(err, bad, 0);
+        int place[RS_ITEMS];
+        rank_keys(key, cnt, p * bits, radix, sm, place);
+        tc::cluster_sync_all();      // every block's counts are there
+        for (int dg = threadIdx.x; dg < radix; dg += RS_THREADS) {
+            int all = 0, before = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                int v;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(tc::map_rank(tot_s + 4 * dg, q)) : "memory");
+                all += v;
+                before += q < rank ? v : 0;
+            }
+            next[dg] = all;
+            earlier[dg] = before;
+        }
+        __syncthreads();
+        scan_digits(next, radix, sm.wsum);
+#pragma unroll
+        for (int e = 0; e < RS_ITEMS; ++e)
+            if (first + e * 32 < cnt) {
+                const int dg = (int)((key[e] >> (p * bits)) & (radix - 1));
+                const int at = next[dg] + earlier[dg] + place[e];
+                ko[at] = key[e];
+                vo[at] = val[e];
+            }
+        tc::cluster_sync_all();      // counts read, pairs written
     }
 }
 
@@ -379,7 +454,7 @@ __global__ void __launch_bounds__(RS_THREADS) rs_scatter_kernel(long long n, lon
         return;
     }
     const int radix = 1 << bits;
-    const SortMem sm = sort_mem(sort_smem, RS_THREADS / 32, radix);
+    const SortMem sm = sort_mem(sort_smem, radix);
     const long long b0 = (long long)blockIdx.x * chunk, b1 = b0 + chunk < n ? b0 + chunk : n;
     const int first = (threadIdx.x >> 5) * (32 * RS_ITEMS) + (threadIdx.x & 31);
     uint32_t key[RS_ITEMS], val[RS_ITEMS];
@@ -489,64 +564,92 @@ __device__ __forceinline__ long long warp_lower_bound(const uint32_t* keys, long
     return lo;
 }
 
-// blockDim = (TX, 128 / TX): TX threads along the column slice, one window per threadIdx.y.
-template <typename TI, typename TO, int VEC>
+// blockDim = (TX, 128 / TX): TX threads along the column slice, one window per threadIdx.y. A thread has NV runs of
+// VEC columns, TX runs apart: 16 bytes of the narrower type in all, so that what a pair costs besides its columns
+// is spread over as many of them where the rows allow only short runs.
+template <typename TI, typename TO, int VEC, int NV>
 __global__ void __launch_bounds__(128) run_sum_kernel(const __grid_constant__ SumArgs a) {
     pdl_wait();
     TO* dT = static_cast<TO*>(a.dT);
     const long long wb = blockIdx.x / a.slices;
     const int slice = (int)(blockIdx.x - wb * a.slices);
     const long long w = wb * blockDim.y + threadIdx.y;
-    const int c = (slice * blockDim.x + threadIdx.x) * VEC;
+    const int c = (slice * NV * blockDim.x + threadIdx.x) * VEC, cstep = blockDim.x * VEC;
     if (w >= a.windows || c >= a.d) return;
     const long long i0 = w * a.P, i1 = i0 + a.P < a.n ? i0 + a.P : a.n;
     const TI* dout = static_cast<const TI*>(a.dout) + c;
     const uint32_t m = (uint32_t)a.m;
-    // the first run of the window is a continuation when the pair before it has the same id
-    bool entering = i0 > 0 && a.keys[i0 - 1] == a.keys[i0];
-    float acc[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
     constexpr int U = 8;
-    for (long long i = i0; i < i1; i += U) {
-        uint32_t key[U + 1];
-        RowRaw<TI, VEC> in[U];
+    // ids and positions one group ahead of the rows they name; id m: no pair
+    uint32_t key[U], val[U], nkey[U], nval[U];
+    auto fetch = [&](long long i, uint32_t(&k)[U], uint32_t(&v)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            key[u] = m;
-            if (i + u < i1) {
-                key[u] = a.keys[i + u];
-                if (key[u] != m) in[u].load(dout + (long long)a.vals[i + u] * a.ldd);
-            }
+            const bool in = i + u < i1;
+            k[u] = in ? a.keys[i + u] : m;
+            v[u] = in ? a.vals[i + u] : 0u;
         }
-        // the key after this group decides whether its last run ends here (m + 1: nothing follows)
-        key[U] = i + U < a.n ? a.keys[i + U] : m;
+    };
+    fetch(i0, key, val);
+    // the first run of the window is a continuation when the pair before it has the same id; the last one goes on
+    // when the pair after the window has
+    const uint32_t before = i0 > 0 ? a.keys[i0 - 1] : m, beyond = i1 < a.n ? a.keys[i1] : m;
+    bool entering = before == key[0];
+    float acc[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
+    for (long long i = i0; i < i1; i += U) {
+        RowRaw<TI, VEC> in[U][NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (key[u] != m) {
+                const TI* p = dout + (long long)val[u] * a.ldd;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    if (j == 0 || c + j * cstep < a.d) in[u][j].load(p + j * cstep);
+            }
+        fetch(i + U, nkey, nval);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i + u >= i1 || key[u] == m) break;
-            float v[VEC];
-            in[u].get(v);
+            if (key[u] == m) break;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] += v[e];
+            for (int j = 0; j < NV; ++j)
+                if (j == 0 || c + j * cstep < a.d) {
+                    float v[VEC];
+                    in[u][j].get(v);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[j][e] += v[e];
+                }
             const bool last_here = i + u + 1 == i1;          // the window's last pair
-            const uint32_t after = last_here ? (i1 < a.n ? a.keys[i1] : m) : key[u + 1];
+            const uint32_t after = last_here ? beyond : u + 1 < U ? key[u + 1 < U ? u + 1 : 0] : nkey[0];
             const bool ends = after != key[u];
             if (!ends && !last_here) continue;
-            if (entering || !ends) {
-                // part of a run that crosses windows
-                float* p = a.partial + (w * 2 + (entering ? 0 : 1)) * a.d + c;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) p[e] = acc[e];
-            } else {
+            for (int j = 0; j < NV; ++j)
+                if (j == 0 || c + j * cstep < a.d) {
+                    if (entering || !ends) {
+                        // part of a run that crosses windows
+                        float* p = a.partial + (w * 2 + (entering ? 0 : 1)) * a.d + c + j * cstep;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) acc[e] *= a.scale;
-                RowRaw<TO, VEC> o;
-                o.set(acc);
-                o.store(dT + (long long)key[u] * a.d + c);
-            }
+                        for (int e = 0; e < VEC; ++e) p[e] = acc[j][e];
+                    } else {
+                        RowRaw<TO, VEC> o;
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) acc[j][e] *= a.scale;
+                        o.set(acc[j]);
+                        o.store(dT + (long long)key[u] * a.d + c + j * cstep);
+                    }
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
+                }
             entering = false;
+        }
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+        for (int u = 0; u < U; ++u) {
+            key[u] = nkey[u];
+            val[u] = nval[u];
         }
     }
 }
@@ -648,14 +751,15 @@ int window_len(long long n, int d) { return n * (long long)d >= (1ll << 24) ? 64
 
 template <typename TI, typename TO, int VEC>
 dlrm_status sum_vec(SumArgs a, cudaStream_t st) {
+    constexpr int W = 16 / (int)(sizeof(TI) < sizeof(TO) ? sizeof(TI) : sizeof(TO)), NV = W / VEC;
     const int runs = a.d / VEC;
-    const int tx = pow2_at_least(runs, 128);
+    const int tx = pow2_at_least((runs + NV - 1) / NV, 128);
     const dim3 block(tx, 128 / tx);
-    a.slices = (runs + tx - 1) / tx;
+    a.slices = (runs + NV * tx - 1) / (NV * tx);
     const long long blocks = (a.windows + block.y - 1) / block.y * a.slices;
     if (blocks > (1ll << 31) - 1) return DLRM_ERR_UNSUPPORTED;
     if (blocks == 0) return DLRM_OK;
-    DLRM_PDL_CHECK(launch_pdl(run_sum_kernel<TI, TO, VEC>, dim3((unsigned)blocks), block, 0, st, a));
+    DLRM_PDL_CHECK(launch_pdl(run_sum_kernel<TI, TO, VEC, NV>, dim3((unsigned)blocks), block, 0, st, a));
     if (a.windows > 1) {
         const unsigned nw = (unsigned)((a.windows - 1 + 7) / 8);
         if (a.d % 4 == 0)
@@ -688,11 +792,10 @@ dlrm_status sum_ti(const SumArgs& a, dlrm_dtype dt, cudaStream_t st) {
     return sum_to<TI, __nv_bfloat16>(a, st);
 }
 
-// 16 warps, 1,024 digits, the pairs of a tile
-constexpr size_t SORT_BYTES_MOST = 2 * 16 * 1024 + 4 * 1024 + 128 + 8 * SORT1_MAX;
+static_assert(sort_bytes(1 << DIG_BITS_MAX) + 2 * 4 * (1 << DIG_BITS_MAX) <= 48 * 1024, "sorting blocks");
 
 struct GradLayout {
-    bool one;               // the one-block sort
+    bool one, eight;        // the one-block sort, the cluster's
     int nblocks, passes, bits;
     long long chunk;
     size_t keys[2], vals[2], hist, partial, total;
@@ -703,6 +806,7 @@ GradLayout grad_layout(long long m, int d, long long n) {
     int kb = 1;
     while ((1ll << kb) <= m) ++kb;             // ids 0 .. m
     L.one = n <= SORT1_MAX;
+    L.eight = !L.one && n <= SORT8_MAX;
     L.passes = (kb + DIG_BITS_MAX - 1) / DIG_BITS_MAX;
     L.bits = std::max(5, (kb + L.passes - 1) / L.passes);
     const long long tiles = (n + RS_TILE - 1) / RS_TILE;
@@ -718,7 +822,7 @@ GradLayout grad_layout(long long m, int d, long long n) {
     const int pairs = L.one ? 1 : 2;
     for (int i = 0; i < 2; ++i) L.keys[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
     for (int i = 0; i < 2; ++i) L.vals[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
-    L.hist = take(!L.one ? sizeof(int) * ((size_t)L.nblocks << L.bits) : 0);
+    L.hist = take(!L.one && !L.eight ? sizeof(int) * ((size_t)L.nblocks << L.bits) : 0);
     const long long windows = (n + window_len(n, d) - 1) / window_len(n, d);
     L.partial = take(sizeof(float) * 2 * (size_t)windows * d);
     L.total = off;
@@ -746,7 +850,7 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
     int* hist = reinterpret_cast<int*>(ws + L.hist);
     const long long bytes = m * d * (long long)(dT_dt == DLRM_F32 ? 4 : 2);
     // launches of the sort: a histogram takes about a third of a scatter's time, and writes so much of the zeros
-    const int shares = L.one ? 1 : 4 * L.passes;
+    const int shares = L.one || L.eight ? 1 : 4 * L.passes;
     long long done = 0;
     auto zeros = [&](int sorters, int share) {
         Zeros z{static_cast<char*>(dT), bytes * done / shares, bytes * (done + share) / shares, sorters};
@@ -757,19 +861,19 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
     auto writers = [&](const Zeros& z) {
         return (unsigned)std::max<long long>(1, std::min<long long>((z.end - z.begin + 16383) / 16384, 2ll * device_sms()));
     };
+    // with the static arrays under 48 KB: 8 warps, up to 1,024 digits, the pairs of a tile
+    const size_t smem = sort_bytes(1 << L.bits);
     int cur = 0;
     if (L.one) {
-        // as many threads as the pairs need at eight each, but enough to write zeros quickly
-        const int threads = n <= 256 * RS_ITEMS ? 256 : SORT1_THREADS;
         const Zeros z = zeros(1, 1);
-        const size_t smem = sort_bytes(threads / 32, 1 << L.bits);
-        cudaFuncSetAttribute(sort_one_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SORT_BYTES_MOST);
-        DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1 + writers(z)), dim3(threads), smem, st, (int)n, m, L.passes,
-                                  L.bits, idx, keys[0], vals[0], err, z));
+        DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1 + writers(z)), dim3(RS_THREADS), smem, st, (int)n, m,
+                                  L.passes, L.bits, idx, keys[0], vals[0], err, z));
+    } else if (L.eight) {
+        const Zeros z = zeros(8, 1);
+        DLRM_PDL_CHECK(launch_pdl(sort_cluster_kernel, dim3(8 + (writers(z) + 7) / 8 * 8), dim3(RS_THREADS), smem, st, (int)n, m,
+                                  L.passes, L.bits, idx, keys[0], vals[0], keys[1], vals[1], err, z));
+        cur = (L.passes - 1) & 1;
     } else {
-        const size_t smem = sort_bytes(RS_THREADS / 32, 1 << L.bits);
-        cudaFuncSetAttribute(rs_scatter_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SORT_BYTES_MOST);
-        cudaFuncSetAttribute(rs_scatter_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SORT_BYTES_MOST);
         const dim3 block(RS_THREADS);
         for (int p = 0; p < L.passes; ++p) {
             const int shift = p * L.bits;
