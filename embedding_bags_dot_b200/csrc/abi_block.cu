@@ -30,6 +30,8 @@ bool spans(int N, int64_t ld, int dt) { return (int64_t)N * ld * (int64_t)elem(d
 dlrm_status experts_sizes(int E, int M, int N, int K) {
     if (E < 1 || M < 0 || N < 1 || K < 1) return DLRM_ERR_INVALID_ARG;
     if (E > DLRM_MAX_EXPERTS) return DLRM_ERR_UNSUPPORTED;
+    // a tile's rows past its expert's last are numbered too
+    if (M > INT31 - 256) return DLRM_ERR_UNSUPPORTED;
     // tiles of one expert are counted in 31 bits
     const int64_t wide = N > K ? N : K;
     if (((int64_t)M / 128 + 1) * (wide / 64 + 1) >= INT31) return DLRM_ERR_UNSUPPORTED;

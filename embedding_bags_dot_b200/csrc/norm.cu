@@ -440,7 +440,7 @@ dlrm_status fwd_vec(const NormFwdArgs& a, cudaStream_t st) {
     constexpr int NV = W / VEC;             // one 16-byte run's elements, however they are loaded
     const int one = norm_threads(a.d, W);
     if (one == 32) {
-        const long long want = (a.rows + 3) / 4, most = 8ll * device_sms();
+        const long long want = (a.rows + 3ll) / 4, most = 8ll * device_sms();
         return norm_launch(rmsnorm_fwd_kernel<T, VEC, NV, false, Q8, 128, false>, (unsigned)std::min(want, most), 128, 0, a, st);
     }
     const long long sms = device_sms();
@@ -492,7 +492,7 @@ dlrm_status bwd_vec(const NormBwdArgs& a, int& nblocks, cudaStream_t st) {
     constexpr int W = 16 / (int)sizeof(T);
     constexpr int NV = W / VEC;
     if (norm_threads(a.d, W) == 32) {
-        nblocks = (int)std::min<long long>((a.rows + 3) / 4, std::min(bwd_resident(128), bwd_most(a.d)));
+        nblocks = (int)std::min<long long>((a.rows + 3ll) / 4, std::min(bwd_resident(128), bwd_most(a.d)));
         const size_t smem = a.partial ? sizeof(float) * 4 * W * 32 : 0;
         return norm_launch(rmsnorm_bwd_kernel<T, VEC, NV, false, 128, false>, nblocks, 128, smem, a, st);
     }

@@ -496,7 +496,7 @@ dlrm_status dlrm_rmsnorm_bwd(int rows, int d, const void* dy, int64_t ld_dy, con
  * W_e = W + e * N * ldw ([N][ldw], as a layer of dlrm_mlp) and rows
  * [offsets[e], offsets[e + 1]) of X and Y:
  *   Y_r = act(X_r W_e^T + bias_e),  fp32 accumulation.
- * Rows outside every expert's range are not written.
+ * Rows outside every expert's range are not written. M <= 2^31 - 256.
  *   offsets  device int32 [E + 1], E <= DLRM_MAX_EXPERTS. A range that decreases,
  *            leaves [0, M] or starts below an earlier offset counts as empty, and
  *            as a bad bag in the error record.

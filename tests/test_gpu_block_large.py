@@ -62,6 +62,24 @@ def test_norm_of_rows_past_32_bits():
     assert float(y[-2].float().min()) == float(torch.tensor(100.0).bfloat16()) == float(y[5].float().max())
 
 
+def test_norm_of_the_most_rows():
+    rows = 2 ** 31 - 1
+    x = torch.full((rows, 1), 3.0, dtype=torch.bfloat16, device="cuda")
+    x[-1], x[2 ** 30] = -3.0, -3.0
+    rstd = torch.zeros(rows, device="cuda")
+    y = torch.zeros_like(x)
+    E.dlrm_rmsnorm_fwd(x, None, y, rstd=rstd, eps=0.0)
+    assert float(y[-1]) == -1.0 == float(y[2 ** 30]) and float(y[-2]) == 1.0
+    assert int((y == 1.0).sum()) == rows - 2
+    third = float(torch.tensor(1.0) / 3.0)
+    assert abs(float(rstd.min()) - third) < 1e-7 > abs(float(rstd.max()) - third)
+    rstd.fill_(2.0)
+    h, dx = torch.zeros_like(x), torch.zeros_like(x)
+    ws = E.alloc_workspace(E.dlrm_rmsnorm_bwd_workspace_size(rows, 1))
+    E.dlrm_rmsnorm_bwd(y, h, rstd, None, dx, ws)           # h = 0: dx = rstd dy
+    assert float(dx[-1]) == -2.0 == float(dx[2 ** 30]) and int((dx == 2.0).sum()) == rows - 2
+
+
 def test_dropout_past_34_bits():
     n = 2 ** 34 + 4 * 1000 + 3                             # the counter's low half passes 32 bits
     x = torch.ones(n, dtype=torch.bfloat16, device="cuda")  # 34 GB, in place

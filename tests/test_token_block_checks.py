@@ -134,6 +134,15 @@ def test_experts_refusals(lib):
         (dict(db=FAKE + 2), bad), (dict(ws=None), wsp), (dict(nws=need - 1), wsp), (dict(ws=FAKE + 8), wsp)])
 
 
+def test_experts_rows_leave_a_tile_below_31_bits(lib):
+    import embedding_bags_dot_b200 as E
+    for M, ok in ((2 ** 31 - 256, True), (2 ** 31 - 255, False), (2 ** 31 - 1, False)):
+        assert (lib.dlrm_experts_bwd_workspace_size(1, M, 8, 8, E.ACT_NONE) > 0) == ok
+        if not ok:
+            assert lib.dlrm_experts_fwd(1, M, 8, 8, FAKE, FAKE, 8, None, E.BF16, FAKE, 8, None, None, E.ACT_NONE, FAKE, 8,
+                                        E.BF16, FAKE, 256, None) == E.ERR_UNSUPPORTED
+
+
 def _raises(status, call, *args, **kw):
     import embedding_bags_dot_b200 as E
     before = E.dlrm_launch_count()
