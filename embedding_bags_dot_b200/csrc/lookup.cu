@@ -11,8 +11,10 @@
 // once; no atomics on values, so the result does not depend on timing.
 //   1. (id, position) pairs are sorted by id, stably: an LSD radix sort whose
 //      digits are as wide as the table needs (two passes up to 2^20 rows), in
-//      one block up to 2,048 pairs, a cluster of eight up to 16,384, else with a
-//      histogram and a scatter launch per pass over blocks of 2,048.
+//      one block up to 2,048 pairs, a cluster of sixteen up to 65,536 (7,375
+//      pairs 15 us the call where blocks of eight with their pairs in memory took
+//      24; 23,517 pairs 19 where four launches took 32), else with a histogram
+//      and a scatter launch per pass over blocks of 2,048.
 //      The sort takes few SMs and little bandwidth, so the other blocks of
 //      its launches write the table's zeros meanwhile; rows with lookups are
 //      written again by the next steps.
@@ -24,7 +26,7 @@
 //      buffer.
 //   3. The partial sums of the crossing runs are added in window order.
 // 65,536 ids into 100,000 x 512 fp32 from bf16: 68 us, of which the sort with
-// the zeros (205 MB) takes about 38, the sums 20 and the join 10; the least bytes
+// the zeros (205 MB) takes about 39, the sums 20 and the join 9; the least bytes
 // would take 41. Calls of a few hundred ids take three launches, 11 us.
 #include <algorithm>
 
@@ -146,7 +148,7 @@ constexpr int RS_WARPS = RS_THREADS / 32;
 constexpr int RS_TILE = RS_THREADS * RS_ITEMS;
 constexpr int RS_BLOCKS_MAX = 296;
 constexpr int SORT1_MAX = RS_TILE;      // pairs the one-block sort takes
-constexpr int SORT8_MAX = 8 * RS_TILE;  // pairs the eight-block cluster's sort takes
+constexpr int SORTC_MAX = 65536;        // pairs a cluster's sort takes
 
 // A share of the table's bytes, zeroed by the blocks of a sorting launch that do not sort.
 struct Zeros {
@@ -182,53 +184,58 @@ __device__ __forceinline__ uint32_t pass_key(const void* in, long long i, long l
     }
 }
 
-// Shared memory of a sorting block (RS_WARPS warps).
+// Shared memory of a sorting block.
 struct SortMem {
-    unsigned short* wc;     // [RS_WARPS][radix]: keys of a digit in each warp, then their places by warp
+    unsigned short* wc;     // [warps][radix]: keys of a digit in each warp, then their places by warp
     int* tot;               // [radix]
     int* wsum;              // [32]
-    uint32_t* keys;         // [tile]: the tile's pairs in order
+    uint32_t* keys;         // [tile]: the tile's pairs in order (the cluster's sort: [tile] of uint2)
     uint32_t* vals;
 };
+template <int WARPS = RS_WARPS>
 __device__ __forceinline__ SortMem sort_mem(unsigned char* p, int radix) {
     SortMem s;
     s.wc = reinterpret_cast<unsigned short*>(p);
-    s.tot = reinterpret_cast<int*>(p + 2 * RS_WARPS * radix);
+    s.tot = reinterpret_cast<int*>(p + 2 * WARPS * radix);
     s.wsum = s.tot + radix;
     s.keys = reinterpret_cast<uint32_t*>(s.wsum + 32);
     s.vals = s.keys + RS_TILE;
     return s;
 }
-constexpr size_t sort_bytes(int radix) { return 2 * (size_t)RS_WARPS * radix + 4 * (size_t)radix + 128 + 8 * (size_t)RS_TILE; }
+constexpr size_t sort_bytes(int radix, int threads = RS_THREADS, int items = RS_ITEMS) {
+    return (size_t)threads / 16 * radix + 4 * (size_t)radix + 128 + 8 * (size_t)threads * items;
+}
 
 // place[e] = how many keys of the block with the same digit come before the thread's e-th; sm.tot[digit] = how many
-// there are. Key e of lane l in warp w is number w * 256 + e * 32 + l of the tile; those from `cnt` on do not count.
+// there are. Key e of lane l in warp w is number (w * ITEMS + e) * 32 + l of the tile; those from `cnt` on do not count.
 // Each warp counts its own keys 32 at a time (equal digits find each other by ballots, 2,400 cycles a block;
 // match.any took 3,400), then each digit's counts
 // are summed over the warps.
-__device__ __forceinline__ void rank_keys(const uint32_t (&key)[RS_ITEMS], int cnt, int shift, int radix, const SortMem& sm,
-                                          int (&place)[RS_ITEMS]) {
+template <int THREADS, int ITEMS>
+__device__ __forceinline__ void rank_keys(const uint32_t (&key)[ITEMS], int cnt, int shift, int radix, const SortMem& sm,
+                                          int (&place)[ITEMS]) {
+    constexpr int WARPS = THREADS / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = warp * (32 * RS_ITEMS) + lane;
-    for (int i = threadIdx.x; i < RS_WARPS * radix / 8; i += RS_THREADS)
+    const int first = warp * (32 * ITEMS) + lane;
+    for (int i = threadIdx.x; i < WARPS * radix / 8; i += THREADS)
         reinterpret_cast<uint4*>(sm.wc)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     unsigned short* mine = sm.wc + warp * radix;
     const unsigned lt = (1u << lane) - 1u;
-    // lanes with the same digit, bit by bit, eight keys side by side; the counts below depend on one another
-    unsigned peers[RS_ITEMS];
+    // lanes with the same digit, bit by bit, all keys side by side; the counts below depend on one another
+    unsigned peers[ITEMS];
 #pragma unroll
-    for (int e = 0; e < RS_ITEMS; ++e) peers[e] = __ballot_sync(0xffffffffu, first + e * 32 < cnt);
+    for (int e = 0; e < ITEMS; ++e) peers[e] = __ballot_sync(0xffffffffu, first + e * 32 < cnt);
     for (int b = 0; 1 << b < radix; ++b) {
 #pragma unroll
-        for (int e = 0; e < RS_ITEMS; ++e) {
+        for (int e = 0; e < ITEMS; ++e) {
             const unsigned bit = (key[e] >> (shift + b)) & 1u;
             const unsigned set = __ballot_sync(0xffffffffu, bit);
             peers[e] &= set ^ (bit - 1u);        // the lanes with this lane's bit
         }
     }
 #pragma unroll
-    for (int e = 0; e < RS_ITEMS; ++e) {
+    for (int e = 0; e < ITEMS; ++e) {
         const bool valid = first + e * 32 < cnt;
         const int dg = (int)((key[e] >> shift) & (radix - 1));
         const int ahead = __popc(peers[e] & lt);
@@ -240,13 +247,13 @@ __device__ __forceinline__ void rank_keys(const uint32_t (&key)[RS_ITEMS], int c
     }
     __syncthreads();
     // two neighbouring digits a thread (one word of counts per warp), all warps' words loaded before any is written
-    for (int d2 = threadIdx.x; d2 < radix / 2; d2 += RS_THREADS) {
+    for (int d2 = threadIdx.x; d2 < radix / 2; d2 += THREADS) {
         uint32_t* col = reinterpret_cast<uint32_t*>(sm.wc) + d2;
-        uint32_t c[RS_WARPS], run = 0;
+        uint32_t c[WARPS], run = 0;
 #pragma unroll
-        for (int w = 0; w < RS_WARPS; ++w) c[w] = col[w * (radix / 2)];
+        for (int w = 0; w < WARPS; ++w) c[w] = col[w * (radix / 2)];
 #pragma unroll
-        for (int w = 0; w < RS_WARPS; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             col[w * (radix / 2)] = run;
             run += c[w];          // both halves at once: a tile's counts stay below 2^16
         }
@@ -255,7 +262,7 @@ __device__ __forceinline__ void rank_keys(const uint32_t (&key)[RS_ITEMS], int c
     }
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < RS_ITEMS; ++e)
+    for (int e = 0; e < ITEMS; ++e)
         if (first + e * 32 < cnt) place[e] += mine[(key[e] >> shift) & (radix - 1)];
 }
 
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(RS_THREADS) sort_one_block_kernel(int n, long 
     report_warp(err, bad, 0);
     for (int p = 0; p < passes; ++p) {
         int place[RS_ITEMS];
-        rank_keys(key, n, p * bits, radix, sm, place);
+        rank_keys<RS_THREADS, RS_ITEMS>(key, n, p * bits, radix, sm, place);
         scan_digits(sm.tot, radix, sm.wsum);
 #pragma unroll
         for (int e = 0; e < RS_ITEMS; ++e)
@@ -345,33 +352,35 @@ __global__ void __launch_bounds__(RS_THREADS) sort_one_block_kernel(int n, long 
     }
 }
 
-// The whole sort in one cluster of eight blocks, 2,048 pairs each: the blocks read one another's digit counts from
-// shared memory, and a cluster barrier stands between passes instead of two launches. The result is in buffer
-// (passes - 1) & 1. The other clusters of the launch write zeros.
-__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(RS_THREADS)
-    sort_cluster_kernel(int n, long long m, int passes, int bits, const int32_t* __restrict__ idx, uint32_t* keys0,
-                        uint32_t* vals0, uint32_t* keys1, uint32_t* vals1, ErrRecord* err,
+// The whole sort in one cluster of sixteen blocks, which keep THREADS * ITEMS pairs each in shared memory, read one
+// another's digit counts there and write each pair to its next place in the block that it falls to. Two cluster
+// barriers a pass stand in for two launches. The other clusters of the launch write zeros.
+constexpr int SORTC_CTAS = 16;
+template <int THREADS, int ITEMS>
+__global__ void __cluster_dims__(SORTC_CTAS, 1, 1) __launch_bounds__(THREADS)
+    sort_cluster_kernel(int n, long long m, int passes, int bits, const int32_t* __restrict__ idx,
+                        uint32_t* __restrict__ keys, uint32_t* __restrict__ vals, ErrRecord* err,
                         const __grid_constant__ Zeros zeros) {
     pdl_wait();
     extern __shared__ __align__(16) unsigned char sort_smem[];
     __shared__ int next[1 << DIG_BITS_MAX], earlier[1 << DIG_BITS_MAX];
-    if (blockIdx.x >= 8) {
+    if (blockIdx.x >= SORTC_CTAS) {
         write_zeros(zeros);
         return;
     }
+    constexpr int TILE = THREADS * ITEMS;
     const int radix = 1 << bits;
-    const SortMem sm = sort_mem(sort_smem, radix);
-    const int rank = (int)tc::cluster_rank(), t0 = rank * RS_TILE;
-    const int cnt = n - t0 < 0 ? 0 : n - t0 < RS_TILE ? n - t0 : RS_TILE;
-    const int first = (threadIdx.x >> 5) * (32 * RS_ITEMS) + (threadIdx.x & 31);
-    const uint32_t tot_s = tc::su32(sm.tot);
-    unsigned bad = 0;
+    const SortMem sm = sort_mem<THREADS / 32>(sort_smem, radix);
+    uint2* pairs = reinterpret_cast<uint2*>(sm.keys);
+    const int rank = (int)tc::cluster_rank(), t0 = rank * TILE;
+    const int cnt = n - t0 < 0 ? 0 : n - t0 < TILE ? n - t0 : TILE;
+    const int first = (threadIdx.x >> 5) * (32 * ITEMS) + (threadIdx.x & 31);
+    const uint32_t tot_s = tc::su32(sm.tot), pairs_s = tc::su32(pairs);
     for (int p = 0; p < passes; ++p) {
-        const uint32_t *kin = p & 1 ? keys0 : keys1, *vin = p & 1 ? vals0 : vals1;
-        uint32_t *ko = p & 1 ? keys1 : keys0, *vo = p & 1 ? vals1 : vals0;
-        uint32_t key[RS_ITEMS], val[RS_ITEMS];
+        uint32_t key[ITEMS], val[ITEMS];
+        unsigned bad = 0;
 #pragma unroll
-        for (int e = 0; e < RS_ITEMS; ++e) {
+        for (int e = 0; e < ITEMS; ++e) {
             const int i = first + e * 32;
             key[e] = val[e] = 0;
             if (i < cnt) {
@@ -380,20 +389,20 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(RS_THREADS)
                     val[e] = (uint32_t)(t0 + i);
                     bad += key[e] == (uint32_t)m;
                 } else {
-                    // written by the cluster's other blocks: from L2
-                    key[e] = __ldcg(kin + t0 + i);
-                    val[e] = __ldcg(vin + t0 + i);
+                    const uint2 kv = pairs[i];
+                    key[e] = kv.x;
+                    val[e] = kv.y;
                 }
             }
         }
         if (p == 0) report_warp(err, bad, 0);
-        int place[RS_ITEMS];
-        rank_keys(key, cnt, p * bits, radix, sm, place);
-        tc::cluster_sync_all();      // every block's counts are there
-        for (int dg = threadIdx.x; dg < radix; dg += RS_THREADS) {
+        int place[ITEMS];
+        rank_keys<THREADS, ITEMS>(key, cnt, p * bits, radix, sm, place);
+        tc::cluster_sync_all();      // every block's counts are there, and its pairs in registers
+        for (int dg = threadIdx.x; dg < radix; dg += THREADS) {
             int all = 0, before = 0;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < SORTC_CTAS; ++q) {
                 int v;
                 asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(tc::map_rank(tot_s + 4 * dg, q)) : "memory");
                 all += v;
@@ -405,14 +414,21 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(RS_THREADS)
         __syncthreads();
         scan_digits(next, radix, sm.wsum);
 #pragma unroll
-        for (int e = 0; e < RS_ITEMS; ++e)
+        for (int e = 0; e < ITEMS; ++e)
             if (first + e * 32 < cnt) {
                 const int dg = (int)((key[e] >> (p * bits)) & (radix - 1));
-                const int at = next[dg] + earlier[dg] + place[e];
-                ko[at] = key[e];
-                vo[at] = val[e];
+                const int at = next[dg] + earlier[dg] + place[e];       // < n: block at / TILE holds it
+                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(
+                                 tc::map_rank(pairs_s + 8 * (at % TILE), at / TILE)),
+                             "r"(key[e]), "r"(val[e])
+                             : "memory");
             }
         tc::cluster_sync_all();      // counts read, pairs written
+    }
+    for (int i = threadIdx.x; i < cnt; i += THREADS) {
+        const uint2 kv = pairs[i];
+        keys[t0 + i] = kv.x;
+        vals[t0 + i] = kv.y;
     }
 }
 
@@ -522,7 +538,7 @@ __global__ void __launch_bounds__(RS_THREADS) rs_scatter_kernel(long long n, lon
         if (t0 > b0) load_tile(t0);
         const int cnt = (int)(b1 - t0 < RS_TILE ? b1 - t0 : RS_TILE);
         int place[RS_ITEMS];
-        rank_keys(key, cnt, shift, radix, sm, place);
+        rank_keys<RS_THREADS, RS_ITEMS>(key, cnt, shift, radix, sm, place);
         scan_digits(sm.tot, radix, sm.wsum);
         // in order of digit through shared memory, so that neighbouring threads write neighbouring pairs
 #pragma unroll
@@ -564,20 +580,24 @@ struct SumArgs {
     void* dT;
 };
 
-// First sorted position with key >= k, by the whole warp: 32 probes at a time.
-__device__ __forceinline__ long long warp_lower_bound(const uint32_t* keys, long long n, long long k, int lane) {
-    long long lo = 0, hi = n;      // the answer is in [lo, hi]
+// How many windows after w begin with `key`, by the whole warp: the 32 next ones at a glance, further ones by their
+// number, 32 probes at a time (the keys are sorted, so these windows follow one another).
+__device__ __forceinline__ long long warp_windows_of(const SumArgs& a, long long w, uint32_t key, int lane) {
+    const long long at = w + 1 + lane;
+    const unsigned same = __ballot_sync(0xffffffffu, at < a.windows && a.keys[at * a.P] == key);
+    if (same != 0xffffffffu) return __popc(same);
+    long long lo = w + 33, hi = a.windows;      // the first window that begins with another key is in [lo, hi]
     while (hi - lo > 0) {
         const long long step = (hi - lo + 31) / 32;
-        const long long at = lo + step * (lane + 1) - 1;     // last element of the lane's piece
-        const bool less = at < hi && (long long)keys[at] < k;
-        const int pieces = __popc(__ballot_sync(0xffffffffu, less));   // pieces wholly below k (sorted keys)
+        const long long last = lo + step * (lane + 1) - 1;              // last window of the lane's piece
+        const bool in = last < hi && a.keys[last * a.P] == key;
+        const int pieces = __popc(__ballot_sync(0xffffffffu, in));      // pieces wholly of this key
         lo += step * pieces;
         if (lo > hi) lo = hi;
         if (step == 1) break;
         hi = lo + step - 1 < hi ? lo + step - 1 : hi;
     }
-    return lo;
+    return lo - w - 1;
 }
 
 // blockDim = (TX, 128 / TX): TX threads along the column slice, one window per threadIdx.y. A thread has NV runs of
@@ -708,10 +728,8 @@ __global__ void __launch_bounds__(256) run_join_kernel(const __grid_constant__ S
         key = a.keys[i1 - 1];
         const uint32_t next = a.keys[i1], first = a.keys[i0], prev = i0 > 0 ? a.keys[i0 - 1] : ~key;
         // it leaves this window, and did not start before it
-        if (key == next && key != (uint32_t)a.m && !(first == key && prev == key)) {
-            const long long end = i1 + warp_lower_bound(a.keys + i1, a.n - i1, (long long)key + 1, threadIdx.x);
-            cnt = (end - 1) / a.P - w;
-        }
+        if (key == next && key != (uint32_t)a.m && !(first == key && prev == key))
+            cnt = warp_windows_of(a, w, key, threadIdx.x);
     }
     float s[VEC];
     auto first_part = [&](long long win) {
@@ -765,9 +783,8 @@ __global__ void __launch_bounds__(256) run_join_kernel(const __grid_constant__ S
 // Pairs per window: short windows while long ones would leave SMs without work.
 int window_len(long long n, int d) { return n * (long long)d >= (1ll << 24) ? 64 : 16; }
 
-template <typename TI, typename TO, int VEC>
-dlrm_status sum_vec(SumArgs a, cudaStream_t st) {
-    constexpr int W = 16 / (int)(sizeof(TI) < sizeof(TO) ? sizeof(TI) : sizeof(TO)), NV = W / VEC;
+template <typename TI, typename TO, int VEC, int NV>
+dlrm_status sum_launch(SumArgs a, cudaStream_t st) {
     const int runs = a.d / VEC;
     const int tx = pow2_at_least((runs + NV - 1) / NV, 128);
     const dim3 block(tx, 128 / tx);
@@ -775,6 +792,9 @@ dlrm_status sum_vec(SumArgs a, cudaStream_t st) {
     const long long blocks = (a.windows + block.y - 1) / block.y * a.slices;
     if (blocks > (1ll << 31) - 1) return DLRM_ERR_UNSUPPORTED;
     if (blocks == 0) return DLRM_OK;
+    // few blocks: a run a thread (288 ids of 19 fp16: 10.6 us the call, 16.9 with eight runs)
+    if constexpr (NV > 1)
+        if (blocks < 2ll * device_sms()) return sum_launch<TI, TO, VEC, 1>(a, st);
     DLRM_PDL_CHECK(launch_pdl(run_sum_kernel<TI, TO, VEC, NV>, dim3((unsigned)blocks), block, 0, st, a));
     if (a.windows > 1) {
         const unsigned nw = (unsigned)((a.windows - 1 + 7) / 8);
@@ -784,6 +804,12 @@ dlrm_status sum_vec(SumArgs a, cudaStream_t st) {
             DLRM_PDL_CHECK(launch_pdl(run_join_kernel<TO, 1>, dim3(nw, (a.d + 31) / 32), dim3(32, 8), 0, st, a));
     }
     return DLRM_OK;
+}
+
+template <typename TI, typename TO, int VEC>
+dlrm_status sum_vec(const SumArgs& a, cudaStream_t st) {
+    constexpr int W = 16 / (int)(sizeof(TI) < sizeof(TO) ? sizeof(TI) : sizeof(TO));
+    return sum_launch<TI, TO, VEC, W / VEC>(a, st);
 }
 
 template <typename TI, typename TO>
@@ -810,8 +836,21 @@ dlrm_status sum_ti(const SumArgs& a, dlrm_dtype dt, cudaStream_t st) {
 
 static_assert(sort_bytes(1 << DIG_BITS_MAX) + 2 * 4 * (1 << DIG_BITS_MAX) <= 48 * 1024, "sorting blocks");
 
+static_assert(SORTC_MAX == SORTC_CTAS * 512 * 8, "the cluster's largest variant");
+template <int THREADS, int ITEMS>
+dlrm_status sort_cluster(dim3 grid, int n, long long m, int passes, int bits, const int32_t* idx, uint32_t* keys,
+                         uint32_t* vals, ErrRecord* err, const Zeros& z, cudaStream_t st) {
+    auto kern = sort_cluster_kernel<THREADS, ITEMS>;
+    // sixteen blocks a cluster, and shared memory past 48 KB, are asked for; always the same values
+    cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sort_bytes(1 << DIG_BITS_MAX, THREADS, ITEMS));
+    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(THREADS), sort_bytes(1 << bits, THREADS, ITEMS), st, n, m, passes, bits, idx,
+                              keys, vals, err, z));
+    return DLRM_OK;
+}
+
 struct GradLayout {
-    bool one, eight;        // the one-block sort, the cluster's
+    bool one, cluster;      // the one-block sort, the cluster's
     int nblocks, passes, bits;
     long long chunk;
     size_t keys[2], vals[2], hist, partial, total;
@@ -822,7 +861,7 @@ GradLayout grad_layout(long long m, int d, long long n) {
     int kb = 1;
     while ((1ll << kb) <= m) ++kb;             // ids 0 .. m
     L.one = n <= SORT1_MAX;
-    L.eight = !L.one && n <= SORT8_MAX;
+    L.cluster = !L.one && n <= SORTC_MAX;
     L.passes = (kb + DIG_BITS_MAX - 1) / DIG_BITS_MAX;
     L.bits = std::max(5, (kb + L.passes - 1) / L.passes);
     const long long tiles = (n + RS_TILE - 1) / RS_TILE;
@@ -835,10 +874,10 @@ GradLayout grad_layout(long long m, int d, long long n) {
         off = align_up(off + bytes, 256);
         return o;
     };
-    const int pairs = L.one ? 1 : 2;
+    const int pairs = L.one || L.cluster ? 1 : 2;
     for (int i = 0; i < 2; ++i) L.keys[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
     for (int i = 0; i < 2; ++i) L.vals[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
-    L.hist = take(!L.one && !L.eight ? sizeof(int) * ((size_t)L.nblocks << L.bits) : 0);
+    L.hist = take(!L.one && !L.cluster ? sizeof(int) * ((size_t)L.nblocks << L.bits) : 0);
     const long long windows = (n + window_len(n, d) - 1) / window_len(n, d);
     L.partial = take(sizeof(float) * 2 * (size_t)windows * d);
     L.total = off;
@@ -866,35 +905,43 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
     int* hist = reinterpret_cast<int*>(ws + L.hist);
     const long long bytes = m * d * (long long)(dT_dt == DLRM_F32 ? 4 : 2);
     // launches of the sort: a histogram takes about a third of a scatter's time, and writes so much of the zeros
-    const int shares = L.one || L.eight ? 1 : 4 * L.passes;
+    const int shares = L.one || L.cluster ? 1 : 4 * L.passes;
     long long done = 0;
     auto zeros = [&](int sorters, int share) {
         Zeros z{static_cast<char*>(dT), bytes * done / shares, bytes * (done + share) / shares, sorters};
         done += share;
         return z;
     };
-    // blocks that write a share's zeros: 16 KB each at least, two per SM at most
-    auto writers = [&](const Zeros& z) {
-        return (unsigned)std::max<long long>(1, std::min<long long>((z.end - z.begin + 16383) / 16384, 2ll * device_sms()));
+    // blocks that write a share's zeros: 16 KB each at least, `most` per SM at most. Eight of the small sorts' blocks
+    // (4,422 ids, 54,642 x 937 fp32: 49 us, 52 with four, 55 with two), two where the sort is as long as the zeros, which
+    // then hold it up (65,536 ids, 100,000 x 512 fp32: 68 us, 71 with four, 72 with eight).
+    auto writers = [&](const Zeros& z, int most) {
+        return (unsigned)std::max<long long>(1, std::min<long long>((z.end - z.begin + 16383) / 16384, (long long)most * device_sms()));
     };
     // with the static arrays under 48 KB: 8 warps, up to 1,024 digits, the pairs of a tile
     const size_t smem = sort_bytes(1 << L.bits);
     int cur = 0;
     if (L.one) {
         const Zeros z = zeros(1, 1);
-        DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1 + writers(z)), dim3(RS_THREADS), smem, st, (int)n, m,
+        DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1 + writers(z, 8)), dim3(RS_THREADS), smem, st, (int)n, m,
                                   L.passes, L.bits, idx, keys[0], vals[0], err, z));
-    } else if (L.eight) {
-        const Zeros z = zeros(8, 1);
-        DLRM_PDL_CHECK(launch_pdl(sort_cluster_kernel, dim3(8 + (writers(z) + 7) / 8 * 8), dim3(RS_THREADS), smem, st, (int)n, m,
-                                  L.passes, L.bits, idx, keys[0], vals[0], keys[1], vals[1], err, z));
-        cur = (L.passes - 1) & 1;
+    } else if (L.cluster) {
+        // the fewest pairs a thread that hold them all: ranking takes longer the more there are
+        const Zeros z = zeros(SORTC_CTAS, 1);
+        const unsigned nw = writers(z, n <= SORTC_CTAS * 256 * 8 ? 8 : 2);
+        const dim3 grid(SORTC_CTAS + (nw + SORTC_CTAS - 1) / SORTC_CTAS * SORTC_CTAS);
+        const dlrm_status r =
+            n <= SORTC_CTAS * 256 * 2   ? sort_cluster<256, 2>(grid, (int)n, m, L.passes, L.bits, idx, keys[0], vals[0], err, z, st)
+            : n <= SORTC_CTAS * 256 * 4 ? sort_cluster<256, 4>(grid, (int)n, m, L.passes, L.bits, idx, keys[0], vals[0], err, z, st)
+            : n <= SORTC_CTAS * 256 * 8 ? sort_cluster<256, 8>(grid, (int)n, m, L.passes, L.bits, idx, keys[0], vals[0], err, z, st)
+                                        : sort_cluster<512, 8>(grid, (int)n, m, L.passes, L.bits, idx, keys[0], vals[0], err, z, st);
+        if (r != DLRM_OK) return r;
     } else {
         const dim3 block(RS_THREADS);
         for (int p = 0; p < L.passes; ++p) {
             const int shift = p * L.bits;
             const Zeros zh = zeros(L.nblocks, 1), zs = zeros(L.nblocks, 3);
-            const dim3 gh(L.nblocks + writers(zh)), gs(L.nblocks + writers(zs));
+            const dim3 gh(L.nblocks + writers(zh, 2)), gs(L.nblocks + writers(zs, 2));
             if (p == 0) {
                 DLRM_PDL_CHECK(launch_pdl(rs_hist_kernel<true>, gh, block, 0, st, n, m, (const void*)idx, shift,
                                           L.bits, L.chunk, hist, err, zh));

@@ -146,3 +146,36 @@ def test_gradient_is_the_adjoint_of_the_lookup():
     E.dlrm_embed_fwd(E.Tables(t.cuda(), [rows], d), 0, idx, out, ws, scale=2.0)
     E.dlrm_embed_bwd(idx, g.cuda(), dt, ws, scale=2.0)
     assert float((out.cpu().double() * g).sum()) == float((t.double() * dt.cpu()).sum())
+
+
+@pytest.mark.parametrize("rows", [40, 5000, 1_500_000])
+@pytest.mark.parametrize("n", [2048, 2049, 8192, 8193, 16_384, 16_385, 32_768, 32_769, 65_535, 65_536, 65_537])
+def test_gradient_at_the_ends_of_each_sort(n, rows):
+    """The one-block, the cluster's and the many-block sort, each of their sizes' ends, one to three digits."""
+    d = 3
+    idx = _ids(n, rows, seed=n + rows, hot=0.2)
+    idx[n // 2] = -1
+    g = torch.Generator().manual_seed(n)
+    dout = torch.randint(-8, 9, (n, d), generator=g).float()
+    ws = E.alloc_workspace(E.dlrm_embed_bwd_workspace_size(rows, d, n))
+    dt = torch.full((rows, d), float("nan"), device="cuda")
+    E.dlrm_embed_bwd(idx.cuda(), dout.cuda(), dt, ws)
+    want = torch.zeros((rows, d), dtype=torch.float64)
+    ok = idx >= 0
+    want.index_add_(0, idx[ok].long(), dout[ok].double())
+    assert torch.equal(dt.cpu().double(), want)             # small integers add exactly
+    assert E.dlrm_check_error(ws) == (E.ERR_INDEX_OOB, 1, 1, 0)
+
+
+@pytest.mark.parametrize("first", [0, 1, 15, 16])
+def test_gradient_of_runs_of_every_number_of_windows(first):
+    """Ids whose runs cover 1 to 3, 31 to 35 and hundreds of windows of 16, begun at every kind of place."""
+    lens = [first] + [1, 15, 16, 17, 33, 31 * 16, 32 * 16 - 1, 32 * 16 + 1, 33 * 16, 33 * 16 + 15, 34 * 16, 35 * 16 + 1, 300 * 16 + 7, 2]
+    idx = torch.repeat_interleave(torch.arange(len(lens)), torch.tensor(lens)).to(torch.int32)
+    g = torch.Generator().manual_seed(first)
+    dout = torch.randint(-8, 9, (len(idx), 8), generator=g).float()
+    perm = torch.randperm(len(idx), generator=g)
+    ws = E.alloc_workspace(E.dlrm_embed_bwd_workspace_size(len(lens), 8, len(idx)))
+    dt = torch.full((len(lens), 8), float("nan"), device="cuda")
+    E.dlrm_embed_bwd(idx[perm].cuda(), dout[perm].cuda(), dt, ws)
+    assert torch.equal(dt.cpu().double(), torch.zeros((len(lens), 8), dtype=torch.float64).index_add_(0, idx.long(), dout.double()))
