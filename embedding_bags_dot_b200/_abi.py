@@ -535,15 +535,16 @@ def _stacked(t, where: str, n: int, rows: int, cols: int):
     """(pointer, row pitch) of [n][rows][cols] whose matrices follow one another at rows * pitch."""
     if t is None:
         return None, cols
-    if t.dim() != 3 or tuple(t.shape) != (n, rows, cols) or (cols > 1 and t.stride(2) != 1):
+    if t.shape != (n, rows, cols):
         _refuse(where)
-    if rows > 1:
-        ld = t.stride(1)
-    else:
-        ld = t.stride(0) if n > 1 else (cols + 15) // 16 * 16
-    if n > 1 and t.stride(0) != rows * ld:
+    lead, ld, step = t.stride()
+    if step != 1 and cols > 1:
         _refuse(where)
-    return _ptr(t), ld
+    if rows == 1:
+        ld = lead if n > 1 else (cols + 15) // 16 * 16
+    if n > 1 and lead != rows * ld:
+        _refuse(where)
+    return (t.data_ptr() if n and rows and cols else None), ld
 
 
 def _vector(t, where: str, dtype, n: int, needed: bool = False):
@@ -555,6 +556,11 @@ def _vector(t, where: str, dtype, n: int, needed: bool = False):
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         _refuse(where)
     return t.data_ptr() if n else None
+
+
+def _space(ws):
+    """(pointer, bytes) of a workspace."""
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
 
 
 _FLOAT_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -615,7 +621,7 @@ def dlrm_embed_fwd(T: Tables, k: int, indices, out, ws, scale: float = 1.0, stre
         _refuse(f)
     dev = _same_device(f, T.data, indices, out, ws)
     return _call(f, dev, stream, T.ref(), int(k), n, idx, float(scale), ptr, ld,
-                 _float_code(out, f), _ptr(ws), _nbytes(ws))
+                 _float_code(out, f), *_space(ws))
 
 
 def dlrm_embed_bwd_workspace_size(rows: int, d: int, n: int) -> int:
@@ -634,7 +640,7 @@ def dlrm_embed_bwd(indices, dout, dtable, ws, scale: float = 1.0, stream=None):
     ptr, ld = _matrix(dout, f, n, d)
     dev = _same_device(f, indices, dout, dtable, ws)
     return _call(f, dev, stream, rows, d, n, idx, float(scale), ptr, ld, _float_code(dout, f),
-                 _ptr(dtable), _float_code(dtable, f), _ptr(ws), _nbytes(ws))
+                 _ptr(dtable), _float_code(dtable, f), *_space(ws))
 
 
 def dlrm_dropout(x, y, p: float, rng, residual=None, stream=None):
@@ -659,13 +665,16 @@ def dlrm_rmsnorm_fwd(x, w, y, eps: float = 1e-6, residual=None, h=None, y_scale=
     if x.dim() != 2:
         _refuse(f)
     rows, d = x.shape
-    for t in (residual, h):
-        if t is not None and t.dtype != x.dtype:
-            _refuse(f)
-    code, ycode = _float_code(x, f), DT_CODE.get(y.dtype)
-    if ycode not in (code, E4M3):
+    dt = x.dtype
+    if (residual is not None and residual.dtype is not dt) or (h is not None and h.dtype is not dt):
         _refuse(f)
-    (px, lx), (pr, lr), (ph, lh), (py, ly) = (_matrix(t, f, rows, d) for t in (x, residual, h, y))
+    code, ycode = _float_code(x, f), DT_CODE.get(y.dtype)
+    if ycode != code and ycode != E4M3:
+        _refuse(f)
+    px, lx = _matrix(x, f, rows, d)
+    pr, lr = _matrix(residual, f, rows, d)
+    ph, lh = _matrix(h, f, rows, d)
+    py, ly = _matrix(y, f, rows, d)
     args = (_vector(w, f, torch.float32, d), float(eps), ph, lh, py, ly, ycode,
             _vector(y_scale, f, torch.float32, rows, ycode == E4M3 and rows > 0), _vector(rstd, f, torch.float32, rows))
     if y_scale is not None and ycode != E4M3:
@@ -687,12 +696,15 @@ def dlrm_rmsnorm_bwd(dy, h, rstd, w, dx, ws, dw=None, dh=None, stream=None):
     if dy.dim() != 2:
         _refuse(f)
     rows, d = dy.shape
-    for t in (h, dx, dh):
-        if t is not None and t.dtype != dy.dtype:
-            _refuse(f)
-    (py, ly), (ph, lh), (pd, ld), (px, lx) = (_matrix(t, f, rows, d) for t in (dy, h, dh, dx))
+    dt = dy.dtype
+    if (h is not None and h.dtype is not dt) or (dx is not None and dx.dtype is not dt) or (dh is not None and dh.dtype is not dt):
+        _refuse(f)
+    py, ly = _matrix(dy, f, rows, d)
+    ph, lh = _matrix(h, f, rows, d)
+    pd, ld = _matrix(dh, f, rows, d)
+    px, lx = _matrix(dx, f, rows, d)
     args = (_vector(rstd, f, torch.float32, rows, True), _vector(w, f, torch.float32, d), pd, ld, _float_code(dy, f), px,
-            lx, _vector(dw, f, torch.float32, d), _ptr(ws), _nbytes(ws))
+            lx, _vector(dw, f, torch.float32, d), *_space(ws))
     dev = _same_device(f, dy, h, rstd, w, dx, dw, dh, ws)
     return _call(f, dev, stream, rows, d, py, ly, ph, lh, *args)
 
@@ -715,7 +727,7 @@ def dlrm_experts_fwd(X, W, offsets, Y, ws, bias=None, act: int = ACT_NONE, x_sca
     pw, lw = _stacked(W, f, n_exp, N, K)
     code = DT_CODE.get(X.dtype, -1)
     args = (_vector(x_scale, f, torch.float32, M), code, pw, lw, _vector(w_scale, f, torch.float32, n_exp * N),
-            _vector(bias, f, torch.float32, n_exp * N), int(act), py, ly, _float_code(Y, f), _ptr(ws), _nbytes(ws))
+            _vector(bias, f, torch.float32, n_exp * N), int(act), py, ly, _float_code(Y, f), *_space(ws))
     dev = _same_device(f, X, W, offsets, Y, ws, bias, x_scale, w_scale)
     return _call(f, dev, stream, n_exp, M, N, K, offs, px, lx, *args)
 
@@ -732,11 +744,15 @@ def dlrm_experts_bwd(dY, X, W, offsets, ws, Y=None, act: int = ACT_NONE, dX=None
     n_exp, M, N, K, offs = _experts_sizes(X, W, offsets, f)
     if dY.dtype != X.dtype or (Y is not None and Y.dtype != X.dtype) or (act == ACT_RELU and Y is None):
         _refuse(f)
-    (pdy, ldy), (py, ly), (px, lx), (pdx, ldx) = (_matrix(t, f, M, c) for t, c in ((dY, N), (Y, N), (X, K), (dX, K)))
-    (pw, lw), (pdw, ldw) = _stacked(W, f, n_exp, N, K), _stacked(dW, f, n_exp, N, K)
+    pdy, ldy = _matrix(dY, f, M, N)
+    py, ly = _matrix(Y, f, M, N)
+    px, lx = _matrix(X, f, M, K)
+    pdx, ldx = _matrix(dX, f, M, K)
+    pw, lw = _stacked(W, f, n_exp, N, K)
+    pdw, ldw = _stacked(dW, f, n_exp, N, K)
     args = (pdy, ldy, py, ly, int(act), px, lx, pw, lw, DT_CODE.get(X.dtype, -1), pdx, ldx,
             F32 if dX is None else _float_code(dX, f), pdw, ldw, F32 if dW is None else _float_code(dW, f),
-            _vector(db, f, torch.float32, n_exp * N), _ptr(ws), _nbytes(ws))
+            _vector(db, f, torch.float32, n_exp * N), *_space(ws))
     dev = _same_device(f, dY, X, W, offsets, ws, Y, dX, dW, db)
     return _call(f, dev, stream, n_exp, M, N, K, offs, *args)
 
