@@ -25,8 +25,8 @@
 //      its row; the parts of a run that crosses windows go to a partial
 //      buffer.
 //   3. The partial sums of the crossing runs are added in window order.
-// 65,536 ids into 100,000 x 512 fp32 from bf16: 68 us, of which the sort with
-// the zeros (205 MB) takes about 39, the sums 20 and the join 9; the least bytes
+// 65,536 ids into 100,000 x 512 fp32 from bf16: 67 us, of which the sort with
+// the zeros (205 MB) takes about 39, the sums 20 and the join 8; the least bytes
 // would take 41. Calls of a few hundred ids take three launches, 11 us.
 #include <algorithm>
 
@@ -690,10 +690,11 @@ __global__ void __launch_bounds__(128) run_sum_kernel(const __grid_constant__ Su
     }
 }
 
-// Adds partial[w + j][0] for j in [j0, j1) to s, in order, eight loads in flight.
+// Adds partial[w + j][0] for j in [j0, j1) to s, in order, 64 bytes of loads in flight at most (four of 16 bytes: 65,536
+// ids of 512 67.0 us the call, 67.7 with eight, 72.3 with sixteen; eight of 4 bytes: 23,517 of 29 18.6, 19.2 with four).
 template <int VEC>
 __device__ __forceinline__ void add_parts(const SumArgs& a, long long w, long long j0, long long j1, int c, float (&s)[VEC]) {
-    constexpr int U = 8;
+    constexpr int U = VEC == 4 ? 4 : 8;
     for (long long j = j0; j < j1; j += U) {
         RowRaw<float, VEC> r[U];
 #pragma unroll
