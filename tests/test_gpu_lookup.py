@@ -179,3 +179,27 @@ def test_gradient_of_runs_of_every_number_of_windows(first):
     dt = torch.full((len(lens), 8), float("nan"), device="cuda")
     E.dlrm_embed_bwd(idx[perm].cuda(), dout[perm].cuda(), dt, ws)
     assert torch.equal(dt.cpu().double(), torch.zeros((len(lens), 8), dtype=torch.float64).index_add_(0, idx.long(), dout.double()))
+
+
+@pytest.mark.parametrize("n", [1000, 5000, 40_000, 80_000])
+def test_captured_gradient_replays_on_new_ids_beside_another_stream(n):
+    rows, d = 3000, 16
+    idx = _ids(n, rows, seed=1).cuda()
+    dout = torch.randint(-8, 9, (n, d)).float().cuda()
+    dt = torch.full((rows, d), float("nan"), device="cuda")
+    ws = E.alloc_workspace(E.dlrm_embed_bwd_workspace_size(rows, d, n))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        E.dlrm_embed_bwd(idx, dout, dt, ws)
+    idx2, other = _ids(n, rows, seed=2).cuda(), torch.cuda.Stream()
+    dt2, ws2 = torch.empty_like(dt), E.alloc_workspace(len(ws))
+    want2 = torch.zeros((rows, d), dtype=torch.float64, device="cuda").index_add_(0, idx2.long(), dout.double())
+    other.wait_stream(torch.cuda.current_stream())
+    for seed in (3, 4):
+        idx.copy_(_ids(n, rows, seed=seed, hot=0.4))
+        graph.replay()
+        E.dlrm_embed_bwd(idx2, dout, dt2, ws2, stream=other)
+        want = torch.zeros((rows, d), dtype=torch.float64, device="cuda").index_add_(0, idx.long(), dout.double())
+        torch.cuda.synchronize()
+        assert torch.equal(dt.double(), want) and torch.equal(dt2.double(), want2)
+        dt.fill_(float("nan"))
