@@ -86,6 +86,26 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float (*red)[32], int sl
     return v;
 }
 
+// rstd of a row whose mean square (with eps) left fp32's ordinary range: from its values times 2^100 or 2^-80 (exact for
+// all that count), whose squares and their sum stay inside. It is at most fp32's largest number (a mean below 2^-256).
+// A row of zeros without eps has 0: its output is zeros, and it adds nothing to a gradient. An infinity or NaN spreads as
+// in other rows. All threads of a row come here together.
+template <int NV, int VEC, bool BLOCK>
+__device__ __forceinline__ float far_rstd(const float (&v)[NV][VEC], bool small, const NormFwdArgs& a, float (*red)[32], int slot) {
+    const float up = small ? 0x1p100f : 0x1p-80f;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float u = v[i][e] * up;
+            ss = fmaf(u, u, ss);
+        }
+    const float mean = fmaf(row_sum<BLOCK>(ss, red, slot), a.inv_d, a.eps * up * up);
+    const float rstd = mean == 0.f ? 0.f : 1.f / sqrtf(mean) * up;
+    return rstd > 3.402823466e38f ? 3.402823466e38f : rstd;
+}
+
 // Rows ahead of the one being reduced are copied into shared memory asynchronously (cp.async): each thread copies
 // the 16-byte runs that it will itself read, so the ring needs no barrier.
 __device__ __forceinline__ void copy16_async(uint4* dst, const void* src) {
@@ -188,7 +208,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 1024 / MAXT) rmsnorm_
         }
         ss = row_sum<BLOCK>(ss, red, slot);
         slot ^= 1;
-        const float rstd = 1.f / sqrtf(fmaf(ss, a.inv_d, a.eps));
+        const float mean = fmaf(ss, a.inv_d, a.eps);
+        float rstd = 1.f / sqrtf(mean);
+        // Squares below 2^-126 lose bits, each at most 2^-150: nothing next to a mean of 2^-100. All threads of the row have
+        // the same mean.
+        if (!(mean >= 0x1p-100f && mean <= 3.402823466e38f)) {
+            rstd = far_rstd<NV, VEC, BLOCK>(v, mean < 1.f, a, red, slot);
+            slot ^= 1;
+        }
         if (a.rstd && t == 0) a.rstd[r] = rstd;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
