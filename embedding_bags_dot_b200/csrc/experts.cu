@@ -289,7 +289,9 @@ __device__ __forceinline__ void ex_promote(float (&acc)[NC][32], uint32_t taddr)
 template <int NC>
 struct EpiRow {
     float bias[NC], wsc[NC], xs;
+    bool far;          // whether any of the warp's scales is neither zero nor within 2^-60 .. 2^60
 };
+__device__ __forceinline__ bool far_scale(float s) { return s != 0.f && !(fabsf(s) >= 0x1p-60f && fabsf(s) <= 0x1p60f); }
 template <int NC, int OP, int KIND>
 __device__ __forceinline__ void ex_fetch(EpiRow<NC>& er, int row0, int nvalid, int j0, int e, const ExpertArgs& a) {
     if constexpr (OP == ET_FWD) {
@@ -302,15 +304,28 @@ __device__ __forceinline__ void ex_fetch(EpiRow<NC>& er, int row0, int nvalid, i
             er.bias[c] = a.bias && in ? __ldg(a.bias + (long long)e * a.J + col) : 0.f;
             er.wsc[c] = KIND == EX_F8 && in ? __ldg(a.w_scale + (long long)e * a.J + col) : 0.f;
         }
+        if constexpr (KIND == EX_F8) {
+            bool far = far_scale(er.xs);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) far |= far_scale(er.wsc[c]);
+            er.far = __any_sync(0xffffffffu, far);
+        }
     }
 }
 
-// Scales, bias and ReLU of 32 columns (group g of the warp's).
+// Scales, bias and ReLU of 32 columns (group g of the warp's). A row's and a column's scale are multiplied first; where
+// their product could leave fp32's range although the result does not, all three factors are multiplied in fp64.
 template <int NC, int KIND>
 __device__ __forceinline__ void ex_affine(float (&v)[32], const EpiRow<NC>& er, int g, const ExpertArgs& a) {
     if constexpr (KIND == EX_F8) {
+        if (er.far) {
 #pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] *= er.xs * __shfl_sync(0xffffffffu, er.wsc[g], q);
+            for (int q = 0; q < 32; ++q)
+                v[q] = (float)((double)v[q] * (double)er.xs * (double)__shfl_sync(0xffffffffu, er.wsc[g], q));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] *= er.xs * __shfl_sync(0xffffffffu, er.wsc[g], q);
+        }
     }
     if (a.bias) {
 #pragma unroll
