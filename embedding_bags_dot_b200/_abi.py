@@ -122,6 +122,7 @@ _SIGS = {
     "dlrm_embed_bwd_workspace_size": (C.c_size_t, [C.c_int64, C.c_int, C.c_int64]),
     "dlrm_embed_bwd": (C.c_int, [C.c_int64, C.c_int, C.c_int64, C.c_void_p, C.c_float, C.c_void_p, C.c_int64, C.c_int,
                                  C.c_void_p, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dlrm_set_sort_clusters": (C.c_int, [C.c_int]),
     "dlrm_dropout": (C.c_int, [C.c_int64, C.c_void_p, C.c_void_p, C.c_int, C.c_double, C.c_void_p, C.c_void_p,
                                C.c_void_p]),
     "dlrm_rmsnorm_fwd": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int, C.c_void_p,
@@ -641,6 +642,11 @@ def dlrm_embed_bwd(indices, dout, dtable, ws, scale: float = 1.0, stream=None):
     dev = _same_device(f, indices, dout, dtable, ws)
     return _call(f, dev, stream, rows, d, n, idx, float(scale), ptr, ld, _float_code(dout, f),
                  _ptr(dtable), _float_code(dtable, f), *_space(ws))
+
+
+def dlrm_set_sort_clusters(allowed: bool) -> None:
+    """Test hook: False makes dlrm_embed_bwd sort as on a device that cannot place its clusters of blocks."""
+    _check(lib().dlrm_set_sort_clusters(int(bool(allowed))), "dlrm_set_sort_clusters")
 
 
 def dlrm_dropout(x, y, p: float, rng, residual=None, stream=None):

@@ -63,6 +63,11 @@ dlrm_status dlrm_embed_fwd(const dlrm_tables* T, int k, int64_t n, const int32_t
                          static_cast<ErrRecord*>(ws), cs(stream));
 }
 
+dlrm_status dlrm_set_sort_clusters(int allowed) {
+    set_sort_clusters(allowed != 0);
+    return DLRM_OK;
+}
+
 size_t dlrm_embed_bwd_workspace_size(int64_t rows, int d, int64_t n) {
     if (rows < 1 || rows >= INT31 || d < 1 || d > MAX_D || n < 0 || n >= INT31) return 0;
     return lookup_grad_workspace(rows, d, n);

@@ -187,6 +187,7 @@ dlrm_status launch_sgd(long long n, float lr, float* w, const float* g, cudaStre
 dlrm_status launch_lookup(const void* table, dlrm_dtype dt, long long rows, int d, long long n, const int32_t* idx,
                           float scale, void* out, long long ldo, dlrm_dtype out_dt, ErrRecord* err, cudaStream_t st);
 size_t lookup_grad_workspace(long long m, int d, long long n);
+void set_sort_clusters(bool allowed);   // test hook behind dlrm_set_sort_clusters
 dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* idx, float scale, const void* dout,
                                long long ldd, dlrm_dtype dt, void* dT, dlrm_dtype dT_dt, char* ws, cudaStream_t st);
 dlrm_status launch_dropout(long long n, const void* x, const void* residual, dlrm_dtype dt, double p,

@@ -13,8 +13,9 @@
 //      digits are as wide as the table needs (two passes up to 2^20 rows), in
 //      one block up to 2,048 pairs, a cluster of sixteen up to 65,536 (7,375
 //      pairs 15 us the call where blocks of eight with their pairs in memory took
-//      24; 23,517 pairs 19 where four launches took 32), else with a histogram
-//      and a scatter launch per pass over blocks of 2,048.
+//      24; 23,517 pairs 19 where four launches took 32), else, and where the
+//      device cannot place sixteen blocks together, with a histogram and a
+//      scatter launch per pass over blocks of 2,048.
 //      The sort takes few SMs and little bandwidth, so the other blocks of
 //      its launches write the table's zeros meanwhile; rows with lookups are
 //      written again by the next steps.
@@ -29,6 +30,7 @@
 // the zeros (205 MB) takes about 39, the sums 20 and the join 8; the least bytes
 // would take 41. Calls of a few hundred ids take three launches, 11 us.
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.cuh"
 #include "rowvec.cuh"
@@ -838,20 +840,53 @@ dlrm_status sum_ti(const SumArgs& a, dlrm_dtype dt, cudaStream_t st) {
 static_assert(sort_bytes(1 << DIG_BITS_MAX) + 2 * 4 * (1 << DIG_BITS_MAX) <= 48 * 1024, "sorting blocks");
 
 static_assert(SORTC_MAX == SORTC_CTAS * 512 * 8, "the cluster's largest variant");
+std::atomic<bool> g_clusters{true};     // dlrm_set_sort_clusters
+
+// Whether the current device can place a cluster of this variant: sixteen blocks are more than every device, partition or
+// context has room for, the largest variant's taking an SM each. Asked once per device; the answer does not change.
+template <int THREADS, int ITEMS>
+bool cluster_fits() {
+    static std::atomic<signed char> known[64];
+    auto kern = sort_cluster_kernel<THREADS, ITEMS>;
+    const int most = (int)sort_bytes(1 << DIG_BITS_MAX, THREADS, ITEMS);
+    int dev = 0;
+    // sixteen blocks a cluster, and shared memory past 48 KB, are asked for; always the same values
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    const bool slot = dev >= 0 && dev < 64;
+    if (slot && known[dev].load(std::memory_order_relaxed)) return known[dev].load(std::memory_order_relaxed) > 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(SORTC_CTAS);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = most;
+    int n = 0;
+    const bool fits = cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+    if (!fits) (void)cudaGetLastError();
+    if (slot) known[dev].store(fits ? 1 : -1, std::memory_order_relaxed);
+    return fits;
+}
+
+// The fewest pairs a thread that hold them all: ranking takes longer the more there are.
+#define DLRM_SORT_CLUSTER(n, CALL)                                        \
+    ((n) <= SORTC_CTAS * 256 * 2   ? CALL(256, 2)                          \
+     : (n) <= SORTC_CTAS * 256 * 4 ? CALL(256, 4)                          \
+     : (n) <= SORTC_CTAS * 256 * 8 ? CALL(256, 8)                          \
+                                   : CALL(512, 8))
+
 template <int THREADS, int ITEMS>
 dlrm_status sort_cluster(dim3 grid, int n, long long m, int passes, int bits, const int32_t* idx, uint32_t* keys,
                          uint32_t* vals, ErrRecord* err, const Zeros& z, cudaStream_t st) {
-    auto kern = sort_cluster_kernel<THREADS, ITEMS>;
-    // sixteen blocks a cluster, and shared memory past 48 KB, are asked for; always the same values
-    cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sort_bytes(1 << DIG_BITS_MAX, THREADS, ITEMS));
-    DLRM_PDL_CHECK(launch_pdl(kern, grid, dim3(THREADS), sort_bytes(1 << bits, THREADS, ITEMS), st, n, m, passes, bits, idx,
-                              keys, vals, err, z));
+    DLRM_PDL_CHECK(launch_pdl(sort_cluster_kernel<THREADS, ITEMS>, grid, dim3(THREADS), sort_bytes(1 << bits, THREADS, ITEMS),
+                              st, n, m, passes, bits, idx, keys, vals, err, z));
     return DLRM_OK;
 }
 
 struct GradLayout {
-    bool one, cluster;      // the one-block sort, the cluster's
+    bool one, cluster;      // the one-block sort; the cluster's where the device can place it
     int nblocks, passes, bits;
     long long chunk;
     size_t keys[2], vals[2], hist, partial, total;
@@ -875,10 +910,11 @@ GradLayout grad_layout(long long m, int d, long long n) {
         off = align_up(off + bytes, 256);
         return o;
     };
-    const int pairs = L.one || L.cluster ? 1 : 2;
+    // the cluster's sizes have the space of the many-block sort, so that the size does not depend on the device
+    const int pairs = L.one ? 1 : 2;
     for (int i = 0; i < 2; ++i) L.keys[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
     for (int i = 0; i < 2; ++i) L.vals[i] = i < pairs ? take(sizeof(uint32_t) * (size_t)n) : 0;
-    L.hist = take(!L.one && !L.cluster ? sizeof(int) * ((size_t)L.nblocks << L.bits) : 0);
+    L.hist = take(!L.one ? sizeof(int) * ((size_t)L.nblocks << L.bits) : 0);
     const long long windows = (n + window_len(n, d) - 1) / window_len(n, d);
     L.partial = take(sizeof(float) * 2 * (size_t)windows * d);
     L.total = off;
@@ -895,11 +931,16 @@ dlrm_status launch_lookup(const void* table, dlrm_dtype dt, long long rows, int 
     return lookup_ti<__nv_bfloat16>(a, out_dt, st);
 }
 
+void set_sort_clusters(bool allowed) { g_clusters.store(allowed, std::memory_order_relaxed); }
+
 size_t lookup_grad_workspace(long long m, int d, long long n) { return grad_layout(m, d, n).total; }
 
 dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* idx, float scale, const void* dout,
                                long long ldd, dlrm_dtype dt, void* dT, dlrm_dtype dT_dt, char* ws, cudaStream_t st) {
-    const GradLayout L = grad_layout(m, d, n);
+    GradLayout L = grad_layout(m, d, n);
+#define DLRM_FITS(T, I) cluster_fits<T, I>()
+    L.cluster = L.cluster && g_clusters.load(std::memory_order_relaxed) && DLRM_SORT_CLUSTER(n, DLRM_FITS);
+#undef DLRM_FITS
     ErrRecord* err = reinterpret_cast<ErrRecord*>(ws);
     uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + L.keys[0]), reinterpret_cast<uint32_t*>(ws + L.keys[1])};
     uint32_t* vals[2] = {reinterpret_cast<uint32_t*>(ws + L.vals[0]), reinterpret_cast<uint32_t*>(ws + L.vals[1])};
@@ -927,15 +968,12 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
         DLRM_PDL_CHECK(launch_pdl(sort_one_block_kernel, dim3(1 + writers(z, 8)), dim3(RS_THREADS), smem, st, (int)n, m,
                                   L.passes, L.bits, idx, keys[0], vals[0], err, z));
     } else if (L.cluster) {
-        // the fewest pairs a thread that hold them all: ranking takes longer the more there are
         const Zeros z = zeros(SORTC_CTAS, 1);
         const unsigned nw = writers(z, n <= SORTC_CTAS * 256 * 8 ? 8 : 2);
         const dim3 grid(SORTC_CTAS + (nw + SORTC_CTAS - 1) / SORTC_CTAS * SORTC_CTAS);
-        const dlrm_status r =
-            n <= SORTC_CTAS * 256 * 2   ? sort_cluster<256, 2>(grid, (int)n, m, L.passes, L.bits, idx, keys[0], vals[0], err, z, st)
-            : n <= SORTC_CTAS * 256 * 4 ? sort_cluster<256, 4>(grid, (int)n, m, L.passes, L.bits, idx, keys[0], vals[0], err, z, st)
-            : n <= SORTC_CTAS * 256 * 8 ? sort_cluster<256, 8>(grid, (int)n, m, L.passes, L.bits, idx, keys[0], vals[0], err, z, st)
-                                        : sort_cluster<512, 8>(grid, (int)n, m, L.passes, L.bits, idx, keys[0], vals[0], err, z, st);
+#define DLRM_SORT(T, I) sort_cluster<T, I>(grid, (int)n, m, L.passes, L.bits, idx, keys[0], vals[0], err, z, st)
+        const dlrm_status r = DLRM_SORT_CLUSTER(n, DLRM_SORT);
+#undef DLRM_SORT
         if (r != DLRM_OK) return r;
     } else {
         const dim3 block(RS_THREADS);

@@ -453,6 +453,11 @@ dlrm_status dlrm_embed_bwd(int64_t rows, int d, int64_t n, const int32_t* indice
                            int64_t ld_dout, dlrm_dtype dout_dt, void* dtable, dlrm_dtype dtable_dt, void* ws,
                            size_t ws_bytes, dlrm_stream stream);
 
+/* Test hook: 0 makes every following dlrm_embed_bwd of the process sort as on a
+ * device that cannot place a cluster of sixteen blocks (where the call finds
+ * that out by itself); 1 restores the default. Results are the same bits. */
+dlrm_status dlrm_set_sort_clusters(int allowed);
+
 /* Dropout with a counter-based generator, over n dense elements of dt:
  *   y[i] = [residual[i] +] (word_i >= p 2^32 ? x[i] / (1 - p) : 0)
  * word_i is 32-bit word i mod 4 of Philox4x32-10 (Salmon et al., "Parallel
