@@ -519,6 +519,21 @@ def _refuse(where: str, status: int = ERR_INVALID_ARG):
     raise DlrmError(status, where)
 
 
+_INT_END = 1 << 31
+
+
+def _counts(where: str, *sizes):
+    """Refuses sizes past C's int: ctypes would pass on their low 32 bits."""
+    if max(sizes) >= _INT_END:
+        _refuse(where, ERR_UNSUPPORTED)
+
+
+def _size_query(name: str, *sizes) -> int:
+    """Bytes that the C query `name` gives for these sizes, 0 where one of them is past C's int."""
+    sizes = [int(v) for v in sizes]
+    return 0 if min(sizes) < 0 or max(sizes) >= _INT_END else int(getattr(lib(), name)(*sizes))
+
+
 def _matrix(t, where: str, rows: int, cols: int):
     """(pointer, row pitch) of a [rows][cols] tensor whose rows are contiguous."""
     if t is None:
@@ -616,6 +631,7 @@ def dlrm_embed_fwd(T: Tables, k: int, indices, out, ws, scale: float = 1.0, stre
     indices: int32 [n]; out: [n][d], fp32, fp16 or bf16."""
     f = "dlrm_embed_fwd"
     n = indices.numel()
+    _counts(f, T.d)
     idx = _vector(indices, f, torch.int32, n)
     ptr, ld = _matrix(out, f, n, T.d)
     if not 0 <= int(k) < T.K or T.data.numel() < sum(T.rows) * (T.d if T.struct.dt != U8ROW else 1):
@@ -626,7 +642,7 @@ def dlrm_embed_fwd(T: Tables, k: int, indices, out, ws, scale: float = 1.0, stre
 
 
 def dlrm_embed_bwd_workspace_size(rows: int, d: int, n: int) -> int:
-    return int(lib().dlrm_embed_bwd_workspace_size(int(rows), int(d), int(n)))
+    return _size_query("dlrm_embed_bwd_workspace_size", rows, d, n)
 
 
 def dlrm_embed_bwd(indices, dout, dtable, ws, scale: float = 1.0, stream=None):
@@ -637,6 +653,7 @@ def dlrm_embed_bwd(indices, dout, dtable, ws, scale: float = 1.0, stream=None):
     if dtable.dim() != 2 or not dtable.is_contiguous():
         _refuse(f)
     rows, d = dtable.shape
+    _counts(f, d)
     idx = _vector(indices, f, torch.int32, n)
     ptr, ld = _matrix(dout, f, n, d)
     dev = _same_device(f, indices, dout, dtable, ws)
@@ -671,6 +688,7 @@ def dlrm_rmsnorm_fwd(x, w, y, eps: float = 1e-6, residual=None, h=None, y_scale=
     if x.dim() != 2:
         _refuse(f)
     rows, d = x.shape
+    _counts(f, rows, d)
     dt = x.dtype
     if (residual is not None and residual.dtype is not dt) or (h is not None and h.dtype is not dt):
         _refuse(f)
@@ -692,7 +710,7 @@ def dlrm_rmsnorm_fwd(x, w, y, eps: float = 1e-6, residual=None, h=None, y_scale=
 
 
 def dlrm_rmsnorm_bwd_workspace_size(rows: int, d: int) -> int:
-    return int(lib().dlrm_rmsnorm_bwd_workspace_size(int(rows), int(d)))
+    return _size_query("dlrm_rmsnorm_bwd_workspace_size", rows, d)
 
 
 def dlrm_rmsnorm_bwd(dy, h, rstd, w, dx, ws, dw=None, dh=None, stream=None):
@@ -702,6 +720,7 @@ def dlrm_rmsnorm_bwd(dy, h, rstd, w, dx, ws, dw=None, dh=None, stream=None):
     if dy.dim() != 2:
         _refuse(f)
     rows, d = dy.shape
+    _counts(f, rows, d)
     dt = dy.dtype
     if (h is not None and h.dtype is not dt) or (dx is not None and dx.dtype is not dt) or (dh is not None and dh.dtype is not dt):
         _refuse(f)
@@ -719,6 +738,7 @@ def _experts_sizes(X, W, offsets, where: str):
     if X.dim() != 2 or W.dim() != 3 or X.shape[1] != W.shape[2] or X.dtype != W.dtype:
         _refuse(where)
     n_exp, N, K = W.shape
+    _counts(where, n_exp, X.shape[0], N, K)
     return n_exp, X.shape[0], N, K, _vector(offsets, where, torch.int32, n_exp + 1, True)
 
 
@@ -739,7 +759,7 @@ def dlrm_experts_fwd(X, W, offsets, Y, ws, bias=None, act: int = ACT_NONE, x_sca
 
 
 def dlrm_experts_bwd_workspace_size(n_experts: int, M: int, N: int, K: int, act: int = ACT_NONE) -> int:
-    return int(lib().dlrm_experts_bwd_workspace_size(int(n_experts), int(M), int(N), int(K), int(act)))
+    return _size_query("dlrm_experts_bwd_workspace_size", n_experts, M, N, K, act)
 
 
 def dlrm_experts_bwd(dY, X, W, offsets, ws, Y=None, act: int = ACT_NONE, dX=None, dW=None, db=None, stream=None):
