@@ -53,7 +53,7 @@ using namespace dlrm;
 extern "C" {
 
 size_t dlrm_row_bytes(int d, dlrm_dtype dt) {
-    if (d < 1) return 0;
+    if (d < 1 || dt == DLRM_E4M3) return 0;      // no tables of 8-bit floating point rows
     if (dt == DLRM_U8ROW) return u8row_bytes(d);
     return (size_t)d * esize(dt);
 }

@@ -109,7 +109,7 @@ typedef struct {
 /* Smallest leading dimension >= n whose rows are 16-byte multiples for dtype dt. */
 int dlrm_ld(int n, dlrm_dtype dt);
 
-/* Bytes of one table row of width d stored as dt (DLRM_U8ROW: the record). */
+/* Bytes of one table row of width d stored as dt (DLRM_U8ROW: the record; DLRM_E4M3: 0, there are no such tables). */
 size_t dlrm_row_bytes(int d, dlrm_dtype dt);
 
 /* Row-wise 8-bit quantisation of `rows` rows of width d (src: device,
