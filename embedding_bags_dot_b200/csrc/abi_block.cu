@@ -69,7 +69,7 @@ dlrm_status dlrm_set_sort_clusters(int allowed) {
 }
 
 size_t dlrm_embed_bwd_workspace_size(int64_t rows, int d, int64_t n) {
-    if (rows < 1 || rows >= INT31 || d < 1 || d > MAX_D || n < 0 || n >= INT31) return 0;
+    if (rows < 1 || rows >= INT31 || d < 1 || d > MAX_D || n < 0 || n >= INT31 || !lookup_grad_fits(d, n)) return 0;
     return lookup_grad_workspace(rows, d, n);
 }
 
@@ -78,7 +78,7 @@ dlrm_status dlrm_embed_bwd(int64_t rows, int d, int64_t n, const int32_t* indice
                            size_t ws_bytes, dlrm_stream stream) {
     if (rows < 1 || d < 1 || n < 0 || n >= INT31 || !float_dt(dout_dt) || !float_dt(dtable_dt))
         return DLRM_ERR_INVALID_ARG;
-    if (rows >= INT31 || d > MAX_D) return DLRM_ERR_UNSUPPORTED;
+    if (rows >= INT31 || d > MAX_D || !lookup_grad_fits(d, n)) return DLRM_ERR_UNSUPPORTED;
     if (!loose(dtable, d, d, dtable_dt)) return DLRM_ERR_INVALID_ARG;
     if (n > 0 && (!indices || !on(indices, 4) || !loose(dout, ld_dout, d, dout_dt))) return DLRM_ERR_INVALID_ARG;
     if (!ws_ok(ws, ws_bytes, lookup_grad_workspace(rows, d, n))) return DLRM_ERR_WORKSPACE;

@@ -186,6 +186,7 @@ dlrm_status launch_sgd(long long n, float lr, float* w, const float* g, cudaStre
 // ---- token blocks: unpooled lookups (lookup.cu), dropout.cu, norm.cu, products grouped by expert (experts.cu)
 dlrm_status launch_lookup(const void* table, dlrm_dtype dt, long long rows, int d, long long n, const int32_t* idx,
                           float scale, void* out, long long ldo, dlrm_dtype out_dt, ErrRecord* err, cudaStream_t st);
+bool lookup_grad_fits(int d, long long n);   // whether the sums' grid does
 size_t lookup_grad_workspace(long long m, int d, long long n);
 void set_sort_clusters(bool allowed);   // test hook behind dlrm_set_sort_clusters
 dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* idx, float scale, const void* dout,

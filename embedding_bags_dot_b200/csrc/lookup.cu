@@ -792,8 +792,7 @@ dlrm_status sum_launch(SumArgs a, cudaStream_t st) {
     const int tx = pow2_at_least((runs + NV - 1) / NV, 128);
     const dim3 block(tx, 128 / tx);
     a.slices = (runs + NV * tx - 1) / (NV * tx);
-    const long long blocks = (a.windows + block.y - 1) / block.y * a.slices;
-    if (blocks > (1ll << 31) - 1) return DLRM_ERR_UNSUPPORTED;
+    const long long blocks = (a.windows + block.y - 1) / block.y * a.slices;      // lookup_grad_fits: below 2^31
     if (blocks == 0) return DLRM_OK;
     // few blocks: a run a thread (288 ids of 19 fp16: 10.6 us the call, 16.9 with eight runs)
     if constexpr (NV > 1)
@@ -932,6 +931,12 @@ dlrm_status launch_lookup(const void* table, dlrm_dtype dt, long long rows, int 
 }
 
 void set_sort_clusters(bool allowed) { g_clusters.store(allowed, std::memory_order_relaxed); }
+
+// A block sums at least one window of at least 512 columns, or all of them.
+bool lookup_grad_fits(int d, long long n) {
+    const long long p = window_len(n, d);
+    return (n + p - 1) / p * ((d + 511) / 512) < 1ll << 31;
+}
 
 size_t lookup_grad_workspace(long long m, int d, long long n) { return grad_layout(m, d, n).total; }
 

@@ -80,3 +80,14 @@ def test_workspace_sizes_of_refused_calls_are_zero():
         for i in range(len(good)):
             for v in (BIG, 2 ** 31, -BIG):
                 assert fn(*good[:i], v, *good[i + 1:]) == 0, (fn.__name__, i, v)
+
+
+def test_a_gradient_of_too_many_blocks_is_refused_before_its_sort():
+    """2^31 - 1 ids of 65,536 columns: more sums than a grid has blocks. Nothing may have been launched by then."""
+    n, d, fake = 2 ** 31 - 1, 65_536, 1 << 20
+    before = E.dlrm_launch_count()
+    status = E.lib().dlrm_embed_bwd(10, d, n, fake, 1.0, fake, d, E.F32, fake, E.F32, fake, 2 ** 62, None)
+    assert status == E.ERR_UNSUPPORTED and E.dlrm_launch_count() == before
+    assert E.dlrm_embed_bwd_workspace_size(10, d, n) == 0
+    # the longest call of each kind that memory can hold is far below
+    assert E.dlrm_embed_bwd_workspace_size(10, 16, n) > 0 and E.dlrm_embed_bwd_workspace_size(10, d, 2 ** 20) > 0
