@@ -275,6 +275,7 @@ extern "C" {
 uint64_t dlrm_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
 dlrm_status dlrm_set_wait_polls(int64_t polls) {
+    set_wait_polls_experts(polls);
     if (set_wait_polls_gemm_tc(polls) != cudaSuccess || set_wait_polls_embbag_mma(polls) != cudaSuccess ||
         set_wait_polls_mlp3(polls) != cudaSuccess ||
         set_wait_polls_embbag_cat(polls) != cudaSuccess || set_wait_polls_interact_tc(polls) != cudaSuccess)

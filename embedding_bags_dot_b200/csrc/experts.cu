@@ -30,7 +30,8 @@
 // finished part to fp32 registers, rounding to nearest, while the next part
 // accumulates in the other TMEM buffer.
 // All waits are bounded: on timeout the kernel records DLRM_ERR_TIMEOUT, drains
-// its copies and MMAs (again bounded), frees TMEM and returns. No multicast load.
+// its copies and MMAs (again bounded), frees TMEM and returns. A warp gives up as one: what follows a wait is issued by
+// all its lanes or by none. No multicast load.
 //
 // Alone, at burst clocks: 16,384 rows by 16 experts of 4,096 x 2,048 in e4m3 108 us
 // (2.5 PFLOP/s, tensor pipe 85 % busy); dX and dW of 16,384 rows by 8 experts of
@@ -41,6 +42,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "kernels.cuh"
@@ -80,6 +82,7 @@ struct ExpertArgs {
     void* C;                  // Y or dX
     long long ldc;
     ErrRecord* err;
+    bool give_up;             // test hook: every warp gives up before its first tile, as if that tile's wait had run out
 };
 
 struct ExpertMaps {
@@ -462,8 +465,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
     const uint32_t tmem = uni(bars->tmem_base);
     volatile int* abort = &bars->abort;
     bool timed_out = false;
-    const int nbj = (a.J + 255) / 256;
-    TileList walk{{rg, a.E, a.rows_out ? nbj : 0, 256, 0}, {rg, OP == EX_BWD ? a.E : 0, nbj, 0, (a.I + 255) / 256}};
+    const int nbj = (a.J + 255) / 256, E = a.give_up ? 0 : a.E;
+    TileList walk{{rg, E, a.rows_out ? nbj : 0, 256, 0}, {rg, OP == EX_BWD ? E : 0, nbj, 0, (a.I + 255) / 256}};
     int mb, cb;
 
     if (warp < 4) {
@@ -514,7 +517,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
                     }
                 }
             }
-            if (timed_out) *abort = 1;
+        timed_out |= a.give_up;
+        if (timed_out) *abort = 1;
             // every load this CTA issued completes before it may exit: the leader's MMA commits release
             // each stage after consuming it (bounded)
             for (int q = 0; q < NS; ++q) {
@@ -568,7 +572,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
                         }
                     }
                 }
-                if (timed_out) *abort = 1;
+        timed_out |= a.give_up;
+        if (timed_out) *abort = 1;
                 if (elect_one()) umma2_commit_both(&bars->drain);
                 __syncwarp();
             }
@@ -599,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
                 for (int x = 0; x < 32; ++x) acc[c][x] = 0.f;
             for (int p = 0; p < parts; ++p, ++part) {
                 const int b = (int)(part & 1u);
-                if (!mbar_wait(&bars->tfull[b], (part >> 1) & 1u, abort)) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->tfull[b], (part >> 1) & 1u, abort))) {
                     timed_out = true;
                     break;
                 }
@@ -618,6 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS2, 1)
                 ex_store<TC, 4, ET_DGRAD, KIND>(acc, er, row0, nvalid, j0, e, a, &maps.c, stage, stage_s);
             }
         }
+        timed_out |= a.give_up;
         if (timed_out) *abort = 1;
         if (lane == 0) bulk_wait_all0();
     }
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = uni(bars->tmem_base);
     volatile int* abort = &bars->abort;
     bool timed_out = false;
-    TileWalk walk{rg, a.E, (a.J + BNT - 1) / BNT, 128, 0};
+    TileWalk walk{rg, a.give_up ? 0 : a.E, (a.J + BNT - 1) / BNT, 128, 0};
     int mb, cb;
 
     if (warp == 0) {
@@ -714,6 +720,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
+        timed_out |= a.give_up;
         if (timed_out) *abort = 1;
         // drain, also when another role gave up: every stage whose load may still be in flight completes its
         // full phase before the CTA may exit (a stage never loaded, or already consumed, passes at once)
@@ -758,6 +765,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
+        timed_out |= a.give_up;
         if (timed_out) *abort = 1;
         if (elect_one()) umma_commit(&bars->drain);
         __syncwarp();
@@ -783,7 +791,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int x = 0; x < 32; ++x) acc[c][x] = 0.f;
             for (int p = 0; p < parts; ++p, ++part) {
                 const int b = (int)(part & 1u);
-                if (!mbar_wait(&bars->tfull[b], (part >> 1) & 1u, abort)) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->tfull[b], (part >> 1) & 1u, abort))) {
                     timed_out = true;
                     break;
                 }
@@ -796,6 +804,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (timed_out) break;
             if (some) ex_store<TC, NC, ET_FWD, KIND>(acc, er, row, nvalid, j0, e, a, &maps.c, stage, stage_s);
         }
+        timed_out |= a.give_up;
         if (timed_out) *abort = 1;
         if (lane == 0) bulk_wait_all0();
     }
@@ -1009,6 +1018,8 @@ __global__ void __launch_bounds__(256) expert_bias_kernel(const __grid_constant_
 
 namespace {
 
+std::atomic<bool> g_give_up{false};     // dlrm_set_wait_polls(0)
+
 bool ex_map(CUtensorMap* m, const void* p, int es, dlrm_dtype dt, int rank, long long inner, long long mid, long long outer,
             long long ld, int box_inner, int box_mid) {
     EncodeTiledFn enc = encode_fn();
@@ -1065,7 +1076,8 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
                                cudaStream_t st) {
     using namespace tc;
     const int es = ex_size(dt), ke = 128 / es;
-    const ExpertArgs a{E, M, N, 0, K, true, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, err};
+    const ExpertArgs a{E, M, N, 0, K, true, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, err,
+                       g_give_up.load(std::memory_order_relaxed)};
     // Tiles of 256 x 256 on SM pairs, or of 128 x 128 or 128 x 64 on single SMs: whichever rounds of tiles take least,
     // by times measured on both sides (us: a round's k-blocks and what it costs besides; the pairs' later start).
     // bf16, 4 experts of 4,096 x 1,024, 8,192 rows: pairs 56, single SMs 70; 512 rows: 12.9 and 12.5; 4 experts of
@@ -1134,7 +1146,8 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
     const bool relu = Y != nullptr;
     const ExpertsLayout L = experts_layout(E, M, N, K, relu);
     ErrRecord* err = reinterpret_cast<ErrRecord*>(ws);
-    ExpertArgs a{E, M, K, dW ? N : 0, N, dX != nullptr, offsets, true, nullptr, nullptr, nullptr, false, dX, lddx, err};
+    ExpertArgs a{E, M, K, dW ? N : 0, N, dX != nullptr, offsets, true, nullptr, nullptr, nullptr, false, dX, lddx, err,
+                 g_give_up.load(std::memory_order_relaxed)};
     float* part = reinterpret_cast<float*>(ws + L.part);
     const void* dP = relu ? (const void*)(ws + L.dp) : dY;
     const long long ldp = relu ? L.ldp : lddy;
@@ -1209,6 +1222,8 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
     DLRM_EX_BWD(__half)
 #undef DLRM_EX_BWD
 }
+
+void set_wait_polls_experts(long long polls) { tc::g_give_up.store(polls == 0, std::memory_order_relaxed); }
 
 bool experts_supported() { return tc::encode_fn() != nullptr; }
 

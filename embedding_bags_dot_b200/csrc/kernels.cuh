@@ -224,6 +224,7 @@ cudaError_t set_wait_polls_gemm_tc(long long polls);
 cudaError_t set_wait_polls_embbag_mma(long long polls);
 cudaError_t set_wait_polls_embbag_cat(long long polls);
 cudaError_t set_wait_polls_interact_tc(long long polls);
+void set_wait_polls_experts(long long polls);   // 0 or not, for every device: an argument of its kernels
 // Every host-side check of dlrm_forward (cat = false) or dlrm_forward_cat (cat = true), ws_bytes included.
 dlrm_status forward_check(const dlrm_tables* T, const dlrm_mlp* bot, const dlrm_mlp* top, int B, const float* dense,
                           const int32_t* offsets, const int32_t* indices, int64_t nnz, const float* y_hat,

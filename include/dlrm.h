@@ -130,7 +130,9 @@ uint64_t dlrm_launch_count(void);
  * many times the first bounded wait of the row-gathering kernels (the bulk
  * copies of a sample's rows), the ordinary waits of the single-CTA
  * tensor-core layer (batches below 4,096 rows) and those of the one-kernel
- * three-layer MLP (the bf16 bottom MLP) poll before giving up;
+ * three-layer MLP (the bf16 bottom MLP) poll before giving up; 0 also makes the
+ * products grouped by expert give up before their first tile, in calls made
+ * from then on for any device (they take no other bound);
  * polls < 0 restores the defaults (about a second). A test sets 0 to make
  * those waits run out at once and checks that the call returns, that
  * dlrm_check_error reports DLRM_ERR_TIMEOUT, and that the next call (after
