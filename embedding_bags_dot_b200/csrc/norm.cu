@@ -86,6 +86,10 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float (*red)[32], int sl
     return v;
 }
 
+// Means below this are taken apart (FAR). Only where eps is below it too: the branch beside the row's registers costs up to
+// a half of odd widths (16,384 x 1,001 bf16 42 us without, 49 with; 4,096 x 10,001: 569, 866).
+constexpr float FAR_MEAN = 0x1p-100f;
+
 // rstd of a row whose mean square (with eps) left fp32's ordinary range: from its values times 2^100 or 2^-80 (exact for
 // all that count), whose squares and their sum stay inside. It is at most fp32's largest number (a mean below 2^-256).
 // A row of zeros without eps has 0: its output is zeros, and it adds nothing to a gradient. An infinity or NaN spreads as
@@ -118,8 +122,9 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 
 constexpr int FWD_RING = 3, BWD_RING = 2;    // rows in the ring: one in use, the others on their way
 
-// Thread t of the row's G threads holds runs t, t + G, ... (NV of them) of VEC elements.
-template <typename T, int VEC, int NV, bool BLOCK, bool Q8, int MAXT, bool RING>
+// Thread t of the row's G threads holds runs t, t + G, ... (NV of them) of VEC elements. FAR: eps is too small to keep
+// every mean above 2^-100, so rows are watched for it.
+template <typename T, int VEC, int NV, bool BLOCK, bool Q8, int MAXT, bool RING, bool FAR>
 __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 1024 / MAXT) rmsnorm_fwd_kernel(const __grid_constant__ NormFwdArgs a) {
     pdl_wait();
     __shared__ float red[4][32];
@@ -208,13 +213,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 1024 / MAXT) rmsnorm_
         }
         ss = row_sum<BLOCK>(ss, red, slot);
         slot ^= 1;
-        const float mean = fmaf(ss, a.inv_d, a.eps);
-        float rstd = 1.f / sqrtf(mean);
-        // Squares below 2^-126 lose bits, each at most 2^-150: nothing next to a mean of 2^-100. All threads of the row have
-        // the same mean.
-        if (!(mean >= 0x1p-100f && mean <= 3.402823466e38f)) {
-            rstd = far_rstd<NV, VEC, BLOCK>(v, mean < 1.f, a, red, slot);
-            slot ^= 1;
+        float rstd;
+        if constexpr (FAR) {
+            const float mean = fmaf(ss, a.inv_d, a.eps);
+            rstd = 1.f / sqrtf(mean);
+            // Squares below 2^-126 lose bits, each at most 2^-150: nothing next to a mean of 2^-100. All threads of the
+            // row have the same mean.
+            if (!(mean >= FAR_MEAN && mean <= 3.402823466e38f)) {
+                rstd = far_rstd<NV, VEC, BLOCK>(v, mean < 1.f, a, red, slot);
+                slot ^= 1;
+            }
+        } else {
+            rstd = 1.f / sqrtf(fmaf(ss, a.inv_d, a.eps));
         }
         if (a.rstd && t == 0) a.rstd[r] = rstd;
 #pragma unroll
@@ -461,35 +471,35 @@ dlrm_status norm_launch(void (*kern)(Args), unsigned grid, int threads, size_t s
     return DLRM_OK;
 }
 
-template <typename T, int VEC, bool Q8>
+template <typename T, int VEC, bool Q8, bool FAR>
 dlrm_status fwd_vec(const NormFwdArgs& a, cudaStream_t st) {
     constexpr int W = 16 / (int)sizeof(T);
     constexpr int NV = W / VEC;             // one 16-byte run's elements, however they are loaded
     const int one = norm_threads(a.d, W);
     if (one == 32) {
         const long long want = (a.rows + 3ll) / 4, most = 8ll * device_sms();
-        return norm_launch(rmsnorm_fwd_kernel<T, VEC, NV, false, Q8, 128, false>, (unsigned)std::min(want, most), 128, 0, a, st);
+        return norm_launch(rmsnorm_fwd_kernel<T, VEC, NV, false, Q8, 128, false, FAR>, (unsigned)std::min(want, most), 128, 0, a, st);
     }
     const long long sms = device_sms();
     // few rows: the latency of a row counts, so it is spread over as many threads as it has runs
     if (a.rows <= sms && one <= 1024)
-        return norm_launch(rmsnorm_fwd_kernel<T, VEC, NV, true, Q8, 1024, false>, (unsigned)a.rows, one, 0, a, st);
+        return norm_launch(rmsnorm_fwd_kernel<T, VEC, NV, true, Q8, 1024, false, FAR>, (unsigned)a.rows, one, 0, a, st);
     // two runs a thread where the runs are whole, else eight elements in smaller pieces (16 of them a thread took
     // 70 us where 8 take 45: 16,384 odd-width bf16 rows)
     constexpr int PT = VEC == W ? 2 * W : 8;
     const int two = norm_threads(a.d, PT);
     if (two > 1024) {
         const int t = norm_threads(a.d, 32);
-        return norm_launch(rmsnorm_fwd_kernel<T, VEC, 32 / VEC, true, Q8, 1024, false>,
+        return norm_launch(rmsnorm_fwd_kernel<T, VEC, 32 / VEC, true, Q8, 1024, false, FAR>,
                            (unsigned)std::min<long long>(a.rows, sms), t, 0, a, st);
     }
     const unsigned grid = (unsigned)std::min<long long>(a.rows, sms * (1024 / two));
     const size_t smem = VEC == W ? (size_t)FWD_RING * 2 * 2 * 16 * two : 0;
-    if (two > 256) return norm_launch(rmsnorm_fwd_kernel<T, VEC, PT / VEC, true, Q8, 1024, VEC == W>, grid, two, smem, a, st);
-    return norm_launch(rmsnorm_fwd_kernel<T, VEC, PT / VEC, true, Q8, 256, VEC == W>, grid, two, smem, a, st);
+    if (two > 256) return norm_launch(rmsnorm_fwd_kernel<T, VEC, PT / VEC, true, Q8, 1024, VEC == W, FAR>, grid, two, smem, a, st);
+    return norm_launch(rmsnorm_fwd_kernel<T, VEC, PT / VEC, true, Q8, 256, VEC == W, FAR>, grid, two, smem, a, st);
 }
 
-template <typename T>
+template <typename T, bool FAR>
 dlrm_status fwd_t(const NormFwdArgs& a, bool q8, cudaStream_t st) {
     Runs u{(int)sizeof(T)};
     u.add(a.x, a.ldx, sizeof(T));
@@ -499,11 +509,16 @@ dlrm_status fwd_t(const NormFwdArgs& a, bool q8, cudaStream_t st) {
     constexpr int W = 16 / (int)sizeof(T);
     int vec = u.vec();
     while (a.d % vec) vec >>= 1;
-    if (vec == W) return q8 ? fwd_vec<T, W, true>(a, st) : fwd_vec<T, W, false>(a, st);
+    if (vec == W) return q8 ? fwd_vec<T, W, true, FAR>(a, st) : fwd_vec<T, W, false, FAR>(a, st);
     if constexpr (W > 4)
-        if (vec == 4) return q8 ? fwd_vec<T, 4, true>(a, st) : fwd_vec<T, 4, false>(a, st);
-    if (vec >= 2) return q8 ? fwd_vec<T, 2, true>(a, st) : fwd_vec<T, 2, false>(a, st);
-    return q8 ? fwd_vec<T, 1, true>(a, st) : fwd_vec<T, 1, false>(a, st);
+        if (vec == 4) return q8 ? fwd_vec<T, 4, true, FAR>(a, st) : fwd_vec<T, 4, false, FAR>(a, st);
+    if (vec >= 2) return q8 ? fwd_vec<T, 2, true, FAR>(a, st) : fwd_vec<T, 2, false, FAR>(a, st);
+    return q8 ? fwd_vec<T, 1, true, FAR>(a, st) : fwd_vec<T, 1, false, FAR>(a, st);
+}
+
+template <typename T>
+dlrm_status fwd_far(const NormFwdArgs& a, bool q8, cudaStream_t st) {
+    return a.eps < FAR_MEAN ? fwd_t<T, true>(a, q8, st) : fwd_t<T, false>(a, q8, st);
 }
 
 // Blocks of `threads` threads that are resident at once: 64 registers a thread above 256 threads, 80 below.
@@ -558,9 +573,9 @@ dlrm_status launch_rmsnorm_fwd(int rows, int d, const void* x, long long ldx, co
                                long long ldy, float* y_scale, float* rstd, cudaStream_t st) {
     const NormFwdArgs a{rows, d, eps, 1.f / (float)d, x, ldx, res, ldres, w, h, ldh, y, ldy, y_scale, rstd};
     const bool q8 = y_scale != nullptr;
-    if (dt == DLRM_F32) return fwd_t<float>(a, q8, st);
-    if (dt == DLRM_F16) return fwd_t<__half>(a, q8, st);
-    return fwd_t<__nv_bfloat16>(a, q8, st);
+    if (dt == DLRM_F32) return fwd_far<float>(a, q8, st);
+    if (dt == DLRM_F16) return fwd_far<__half>(a, q8, st);
+    return fwd_far<__nv_bfloat16>(a, q8, st);
 }
 
 size_t rmsnorm_bwd_partial_floats(int rows, int d) { return (size_t)std::min<long long>(rows, bwd_most(d)) * d; }

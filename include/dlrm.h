@@ -475,10 +475,11 @@ dlrm_status dlrm_dropout(int64_t n, const void* x, const void* residual, dlrm_dt
 
 /* Root-mean-square norm with the residual's addition, per row of d <= 32,768:
  *   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * w
- * in fp32 from the unrounded h, also where h^2 alone would leave fp32's range
- * (|h| up to the largest number and down to the smallest). rstd is at most
- * fp32's largest number, and 0 for a row of zeros under eps = 0, whose y is
- * zeros and which adds nothing to a gradient.
+ * in fp32 from the unrounded h. A sum of squares past fp32's largest number (one
+ * |h| above 1.8e19, or less in wide rows) makes rstd 0 and y zeros. Under an eps
+ * below 2^-100 such rows, and rows whose squares are too small for fp32, are
+ * held exactly: rstd is at most fp32's largest number, and 0 for a row of zeros
+ * under eps = 0, whose y is zeros and which adds nothing to a gradient.
  *   x, residual (optional), h (optional): [rows][ld] of dt (fp32, fp16, bf16);
  *     h may be x's or residual's own buffer
  *   w        fp32 [d], or NULL for ones;  eps >= 0

