@@ -81,6 +81,8 @@ struct ExpertArgs {
     bool relu;
     void* C;                  // Y or dX
     long long ldc;
+    void* D;                  // dW
+    long long ldd;
     ErrRecord* err;
     bool give_up;             // test hook: every warp gives up before its first tile, as if that tile's wait had run out
 };
@@ -342,8 +344,9 @@ __device__ __forceinline__ void ex_affine(float (&v)[32], const EpiRow<NC>& er, 
 }
 
 // One warp's share of a finished tile: 32 rows (one per lane) x 32 NC columns from column j0. Rows go out
-// through the warp's 4 KB stage, 128 bytes of columns at a time: whole 32-row groups by TMA (columns
-// past J are clipped), a group that holds the expert's last row by 16-byte stores of its valid rows only.
+// through the warp's 4 KB stage, 128 bytes of columns at a time: whole 32-row groups by TMA, a group that holds the
+// expert's last row by 16-byte stores of its valid rows only. So are the last columns of a width that is no multiple of 16
+// bytes: TMA clips a box there, and would write zeros over up to 15 bytes beside the matrix.
 //   row0: first output row of the warp; nvalid: its rows that exist (<= 0: none); e: expert
 template <typename TC, int NC, int OP, int KIND>
 __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>& er, int row0, int nvalid, int j0, int e,
@@ -382,7 +385,8 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>&
             }
             *reinterpret_cast<uint4*>(row + 16 * (q ^ (lane & 7))) = w;
         }
-        if (OP == ET_WGRAD || nvalid >= 32) {
+        const bool clipped = n0 + CW > a.J && a.J % (16 / (int)sizeof(TC)) != 0;
+        if ((OP == ET_WGRAD || nvalid >= 32) && !clipped) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
@@ -398,7 +402,8 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>&
                 const int col = n0 + q * E16;
                 if (r < nvalid && col < a.J) {
                     const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + 16 * (q ^ (r & 7)));
-                    TC* dst = static_cast<TC*>(a.C) + (long long)(row0 + r) * a.ldc + col;
+                    TC* dst = OP == ET_WGRAD ? static_cast<TC*>(a.D) + ((long long)e * a.I + row0 + r) * a.ldd + col
+                                             : static_cast<TC*>(a.C) + (long long)(row0 + r) * a.ldc + col;
                     if (col + E16 <= a.J) {
                         *reinterpret_cast<uint4*>(dst) = w;
                     } else {
@@ -1076,7 +1081,7 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
                                cudaStream_t st) {
     using namespace tc;
     const int es = ex_size(dt), ke = 128 / es;
-    const ExpertArgs a{E, M, N, 0, K, true, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, err,
+    const ExpertArgs a{E, M, N, 0, K, true, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, nullptr, 0, err,
                        g_give_up.load(std::memory_order_relaxed)};
     // Tiles of 256 x 256 on SM pairs, or of 128 x 128 or 128 x 64 on single SMs: whichever rounds of tiles take least,
     // by times measured on both sides (us: a round's k-blocks and what it costs besides; the pairs' later start).
@@ -1146,7 +1151,7 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
     const bool relu = Y != nullptr;
     const ExpertsLayout L = experts_layout(E, M, N, K, relu);
     ErrRecord* err = reinterpret_cast<ErrRecord*>(ws);
-    ExpertArgs a{E, M, K, dW ? N : 0, N, dX != nullptr, offsets, true, nullptr, nullptr, nullptr, false, dX, lddx, err,
+    ExpertArgs a{E, M, K, dW ? N : 0, N, dX != nullptr, offsets, true, nullptr, nullptr, nullptr, false, dX, lddx, dW, lddw, err,
                  g_give_up.load(std::memory_order_relaxed)};
     float* part = reinterpret_cast<float*>(ws + L.part);
     const void* dP = relu ? (const void*)(ws + L.dp) : dY;
