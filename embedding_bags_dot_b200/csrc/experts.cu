@@ -345,8 +345,9 @@ __device__ __forceinline__ void ex_affine(float (&v)[32], const EpiRow<NC>& er, 
 
 // One warp's share of a finished tile: 32 rows (one per lane) x 32 NC columns from column j0. Rows go out
 // through the warp's 4 KB stage, 128 bytes of columns at a time: whole 32-row groups by TMA, a group that holds the
-// expert's last row by 16-byte stores of its valid rows only. So are the last columns of a width that is no multiple of 16
-// bytes: TMA clips a box there, and would write zeros over up to 15 bytes beside the matrix.
+// expert's last row by 16-byte stores of its valid rows only. TMA clips a box at 16 bytes: of a width that is no multiple
+// of that it has the columns before, and the others go out one by one (by TMA they would take up to 15 bytes beside the
+// matrix with them).
 //   row0: first output row of the warp; nvalid: its rows that exist (<= 0: none); e: expert
 template <typename TC, int NC, int OP, int KIND>
 __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>& er, int row0, int nvalid, int j0, int e,
@@ -385,25 +386,36 @@ __device__ __forceinline__ void ex_store(float (&acc)[NC][32], const EpiRow<NC>&
             }
             *reinterpret_cast<uint4*>(row + 16 * (q ^ (lane & 7))) = w;
         }
-        const bool clipped = n0 + CW > a.J && a.J % (16 / (int)sizeof(TC)) != 0;
-        if ((OP == ET_WGRAD || nvalid >= 32) && !clipped) {
+        constexpr int E16 = 16 / (int)sizeof(TC);
+        auto out = [&](int r, int col) {
+            return OP == ET_WGRAD ? static_cast<TC*>(a.D) + ((long long)e * a.I + row0 + r) * a.ldd + col
+                                  : static_cast<TC*>(a.C) + (long long)(row0 + r) * a.ldc + col;
+        };
+        if (OP == ET_WGRAD || nvalid >= 32) {
+            const int whole = a.J / E16 * E16;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && n0 < whole) {
                 if constexpr (OP == ET_WGRAD) ex_store_3d(mapC, stage_s, n0, row0, e);
                 else tma_store_2d(mapC, stage_s, n0, row0);
             }
+            if (whole < a.J && n0 + CW > whole && lane < nvalid) {
+                const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * (((whole - n0) / E16) ^ (lane & 7)));
+                const TC* src = reinterpret_cast<const TC*>(&w);
+                TC* dst = out(lane, whole);
+#pragma unroll
+                for (int k = 0; k < E16 - 1; ++k)
+                    if (whole + k < a.J) dst[k] = src[k];
+            }
         } else {
             __syncwarp();
-            constexpr int E16 = 16 / (int)sizeof(TC);
 #pragma unroll
             for (int it = 0; it < 8; ++it) {
                 const int r = it * 4 + (lane >> 3), q = lane & 7;
                 const int col = n0 + q * E16;
                 if (r < nvalid && col < a.J) {
                     const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + 16 * (q ^ (r & 7)));
-                    TC* dst = OP == ET_WGRAD ? static_cast<TC*>(a.D) + ((long long)e * a.I + row0 + r) * a.ldd + col
-                                             : static_cast<TC*>(a.C) + (long long)(row0 + r) * a.ldc + col;
+                    TC* dst = out(r, col);
                     if (col + E16 <= a.J) {
                         *reinterpret_cast<uint4*>(dst) = w;
                     } else {
@@ -1042,6 +1054,9 @@ bool ex_map(CUtensorMap* m, const void* p, int es, dlrm_dtype dt, int rank, long
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Columns of an output's map: whole runs of 16 bytes (a map has at least one; of narrower outputs TMA stores nothing).
+long long ex_whole(long long cols, int es) { return std::max<long long>(cols * es / 16, 1) * (16 / es); }
+
 int ex_size(dlrm_dtype dt) { return dt == DLRM_F32 ? 4 : dt == DLRM_E4M3 ? 1 : 2; }
 
 // Most tiles a call can have: row blocks of every expert, the experts with rows being at most min(E, M).
@@ -1106,7 +1121,7 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
     if ((!only32 && !ex_map(&maps.a, X, es, dt, 2, K, M, 1, ldx, ke, 128)) ||
         (!pair && !ex_map(&maps.a32, X, es, dt, 2, K, M, 1, ldx, ke, 32)) ||
         !ex_map(&maps.b, W, es, dt, 3, K, N, E, ldw, ke, pair || !narrow ? 128 : 64) ||
-        !ex_map(&maps.c, Y, ex_size(y_dt), y_dt, 2, N, M, 1, ldy, 128 / ex_size(y_dt), 32))
+        !ex_map(&maps.c, Y, ex_size(y_dt), y_dt, 2, ex_whole(N, ex_size(y_dt)), M, 1, ldy, 128 / ex_size(y_dt), 32))
         return DLRM_ERR_CUDA;
     const int fmt = dt == DLRM_BF16 ? 1 : 0;
 #define DLRM_EX_FWD(TC, KIND)                                                                     \
@@ -1163,7 +1178,7 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
     a.rows_out = dX && M > 0;
     if (a.rows_out) {
         if (!ex_map(&maps.a, dP, 2, dt, 2, N, M, 1, ldp, 64, 128) || !ex_map(&maps.b, W, 2, dt, 3, K, N, E, ldw, 64, 64) ||
-            !ex_map(&maps.c, dX, ex_size(dx_dt), dx_dt, 2, K, M, 1, lddx, 128 / ex_size(dx_dt), 32))
+            !ex_map(&maps.c, dX, ex_size(dx_dt), dx_dt, 2, ex_whole(K, ex_size(dx_dt)), M, 1, lddx, 128 / ex_size(dx_dt), 32))
             return DLRM_ERR_CUDA;
         tiles += most_tiles(E, M, 256, nbk);
     }
@@ -1176,7 +1191,7 @@ dlrm_status launch_experts_bwd(int E, int M, int N, int K, const int32_t* offset
             !ex_map(&maps.wb, pb, 2, dt, 2, K, rows, 1, M > 0 ? ldx : L.ldtx, 64, 64) ||
             !ex_map(&maps.at, ws + L.tail_dp, 2, dt, 3, N, PREP_ROWS, E, L.ldp, 64, 64) ||
             !ex_map(&maps.bt, ws + L.tail_x, 2, dt, 3, K, PREP_ROWS, E, L.ldtx, 64, 64) ||
-            !ex_map(&maps.wc, dW, ex_size(dw_dt), dw_dt, 3, K, N, E, lddw, 128 / ex_size(dw_dt), 32))
+            !ex_map(&maps.wc, dW, ex_size(dw_dt), dw_dt, 3, ex_whole(K, ex_size(dw_dt)), N, E, lddw, 128 / ex_size(dw_dt), 32))
             return DLRM_ERR_CUDA;
         tiles += (long long)E * ((N + 255) / 256) * nbk;
     }
