@@ -8,9 +8,11 @@
 // kept when its word is at least p * 2^32 (rounded to an integer), so the
 // probability is right to 2^-33.
 //
-// Bound by memory with fp32 elements or a residual (33.5 M bf16 with residual:
-// 34 us, 5.9 TB/s), by the integer pipe without (31 us, 4.4 TB/s): ten rounds
-// of two 32 x 32 -> 64 products serve four elements. Each thread takes two runs
+// Bound by memory with fp32 elements (33.5 M: 41 us, 6.5 TB/s) or a residual
+// (33.5 M bf16: 34 to 38 us, 5.3 to 5.9 TB/s), by integer work without (31 us,
+// 4.4 TB/s): ten rounds of two 32 x 32 -> 64 products serve four elements, and
+// the pipe of wide products is the busiest (65 % of the time, DRAM 32 %, issue
+// 58 %). Each thread takes two runs
 // of 16 bytes at a time (four or eight elements, one or two generator calls
 // each). seed and offset are read from
 // device memory so that a captured graph draws anew when they are changed
@@ -123,7 +125,8 @@ dlrm_status launch_t(const DropArgs& a, cudaStream_t st) {
     const bool al = rows_on(a.x, 0, 16) && rows_on(a.y, 0, 16) && rows_on(a.residual, 0, 16);
     const int vec = al ? 16 / (int)sizeof(T) : 4;
     const long long want = (a.n + 512ll * vec - 1) / (512ll * vec);
-    // many short blocks: one wave of 8 an SM measured 38.7 us where 40 take 34.3 (33.5 M bf16 with residual)
+    // many short blocks: 40 an SM where one wave of five, eight, 16 or 80 take longer (33.5 M: bf16 with residual 34.1 us and
+    // 36.2, 35.3, 34.8, 34.5; without 30.5 and 32.3, 31.1, 30.6, 31.2; fp32 41.2 and 43.6, 50.5, 42.6, 41.6)
     const long long most = 40ll * device_sms();
     const dim3 grid((unsigned)(want < most ? want : most));
     const bool small = a.n <= 4ll << 32;

@@ -37,8 +37,8 @@
 // (2.5 PFLOP/s, tensor pipe 85 % busy); dX and dW of 16,384 rows by 8 experts of
 // 4,096 x 1,024 in bf16 198 us (1.39 PFLOP/s, 87 %), after 75 us of masking dY and
 // summing the bias gradient (5.4 TB/s). Back to back at the 1,000 W cap 137 to 147
-// and 326 us. 12 rows by 8 experts of 4,096 x 1,024: 11 to 15 us, the weights'
-// 67 MB at up to 6 TB/s.
+// and 326 us. 12 rows by 8 experts of 4,096 x 1,024: 12 to 15 us for the weights of
+// the four to six experts that had rows, 34 to 50 MB, at 3 to 3.5 TB/s; in e4m3 11.
 #include <cuda.h>
 
 #include <algorithm>
@@ -1099,10 +1099,13 @@ dlrm_status launch_experts_fwd(int E, int M, int N, int K, const int32_t* offset
     const ExpertArgs a{E, M, N, 0, K, true, offsets, true, bias, x_scale, w_scale, relu, Y, ldy, nullptr, 0, err,
                        g_give_up.load(std::memory_order_relaxed)};
     // Tiles of 256 x 256 on SM pairs, or of 128 x 128 or 128 x 64 on single SMs: whichever rounds of tiles take least,
-    // by times measured on both sides (us: a round's k-blocks and what it costs besides; the pairs' later start).
-    // bf16, 4 experts of 4,096 x 1,024, 8,192 rows: pairs 56, single SMs 70; 512 rows: 12.9 and 12.5; 4 experts of
-    // 1,024 x 4,096, 4,096 rows: 29 and 37, 2,048 rows: 26 and 21. 12 rows of 8 experts of 4,096 x 1,024: 13.6 at 128
-    // columns, 15.5 at 64 (and 17.6 at 32: a k-block's issue costs 420 to 465 cycles at any width).
+    // by times of whole rounds (us: a round's k-blocks and what it costs besides; the pairs' later start). Short reductions
+    // and calls of few rounds take up to twice as long as these say, all shapes alike, so the choice holds. Measured
+    // (pairs; 128 columns; 64): 4 experts of 4,096 x 1,024 bf16, 8,192 rows 57, 71, 106, 512 rows 15.6, 15.0, 16.0;
+    // 4 of 1,024 x 4,096, 4,096 rows 35, 37, 58, 2,048 rows 26, 21, 32; 8 of 4,096 x 1,024, 64 rows 19.6, 16.0, 19.3,
+    // 12 rows 19.9, 14.8, 15.7 (and 17.6 at 32 columns beside 13.6 at 128 then: a k-block's issue costs 420 to 465 cycles
+    // at any width); 24 of 1,024 x 479 fp16, 20,000 rows 26.7, 31.3, 41.4; 8 of 2,048 x 256, 5,000 rows 14.9, 12.5, 16.2;
+    // 16 of 4,096 x 2,048 e4m3, 16,384 rows 127, 154, 227, 1,000 rows 35.7, 30.8, 36.8.
     const long long sms = device_sms(), used = std::min(E, M);
     const double nk = (K + ke - 1) / ke;
     auto rounds = [&](long long rows_per, long long cols, long long units) {

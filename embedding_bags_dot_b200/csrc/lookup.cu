@@ -21,14 +21,20 @@
 //      written again by the next steps.
 //   2. The sorted pairs are cut into windows of fixed length, each summed by
 //      one group of threads per column slice, whatever rows they belong to, so
-//      a row looked up thousands of times costs no more per lookup than any
-//      other. A run of equal ids inside a window is final and goes straight to
-//      its row; the parts of a run that crosses windows go to a partial
-//      buffer.
-//   3. The partial sums of the crossing runs are added in window order.
+//      that here a row looked up thousands of times costs no more per lookup
+//      than any other. A run of equal ids inside a window is final and goes
+//      straight to its row; the parts of a run that crosses windows go to a
+//      partial buffer.
+//   3. The partial sums of the crossing runs are added in window order, a run's
+//      by one block per column slice. Here one id's share counts: all of 65,536
+//      ids the same take 49 us at 512 columns where spread ids take 44, 60 at 8
+//      columns where those take 28; all of 1,000,000 630 at 8 columns (80), 547
+//      at 512 (268).
 // 65,536 ids into 100,000 x 512 fp32 from bf16: 67 us, of which the sort with
 // the zeros (205 MB) takes about 39, the sums 20 and the join 8; the least bytes
-// would take 41. Calls of a few hundred ids take three launches, 11 us.
+// would take 41. Calls of a few hundred ids take three launches, 11 us. Past the
+// cluster's sort: 131,072 ids into the same 94 us (52), 1,000,000 ids into
+// 100,000 x 64 107 us (24).
 #include <algorithm>
 #include <atomic>
 
@@ -783,7 +789,9 @@ __global__ void __launch_bounds__(256) run_join_kernel(const __grid_constant__ S
     }
 }
 
-// Pairs per window: short windows while long ones would leave SMs without work.
+// Pairs per window: short windows while long ones would leave SMs without work. us a call with 16 and with 64, at n * d of
+// 2^22 22.5 and 28.3; 2^23 31 and 34 to 35; 2^24 41 and 39, 38 and 40, 49 and 45 (1,024, 256, 64 columns); 2^25 53 and 47,
+// 74 and 67.
 int window_len(long long n, int d) { return n * (long long)d >= (1ll << 24) ? 64 : 16; }
 
 template <typename TI, typename TO, int VEC, int NV>
@@ -959,9 +967,9 @@ dlrm_status launch_lookup_grad(long long m, int d, long long n, const int32_t* i
         done += share;
         return z;
     };
-    // blocks that write a share's zeros: 16 KB each at least, `most` per SM at most. Eight of the small sorts' blocks
-    // (4,422 ids, 54,642 x 937 fp32: 49 us, 52 with four, 55 with two), two where the sort is as long as the zeros, which
-    // then hold it up (65,536 ids, 100,000 x 512 fp32: 68 us, 71 with four, 72 with eight).
+    // blocks that write a share's zeros: 16 KB each at least, `most` per SM at most. Eight of the small sorts' blocks, two
+    // where the sort is as long as the zeros, which then hold it up. us a call with eight and with two, into 100,000 x 512
+    // fp32: 2,500 ids 41 and 46, 8,192 46 and 51, 32,768 56 and 60; 32,769 65 and 62, 50,000 67 and 65, 65,536 70 and 67.
     auto writers = [&](const Zeros& z, int most) {
         return (unsigned)std::max<long long>(1, std::min<long long>((z.end - z.begin + 16383) / 16384, (long long)most * device_sms()));
     };

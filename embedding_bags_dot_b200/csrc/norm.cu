@@ -9,12 +9,18 @@
 //   dx = rstd * (g - xh * mean_c(g xh)) + dh,      dw_c = sum_rows dy_c xh_c.
 //
 // Both passes move each row once, so memory bounds them, with instruction issue
-// close behind (16,384 x 4,096 bf16 to e4m3 with residual: 78 us, 6.0 TB/s, 77 %
-// of issue slots; backward of 20,000 x 2,040 fp16: 67 us, 4.9 TB/s). A row's
-// elements stay in registers between the statistics and the output. A warp takes
-// rows of up to one run per lane (no block barrier), a block longer ones, two
-// runs per thread; where rows allow whole 16-byte runs the next rows are on
-// their way to shared memory meanwhile. Blocks are as many as fit at once; they
+// close behind (16,384 x 4,096 bf16 to e4m3 with residual: 78 to 84 us, 5.6 to
+// 6.0 TB/s, 77 % of issue slots; backward of 20,000 x 2,040 fp16: 65 to 67 us,
+// 4.9 TB/s). A row's elements stay with their threads between the statistics and
+// the output. A warp takes rows of up to one run per lane (no block barrier), a
+// block longer ones, two runs per thread; where rows allow whole 16-byte runs the
+// next rows are on their way to shared memory meanwhile. Rows of more than 16,384
+// 16-bit or 8,192 other elements (fp32, and widths without whole runs) take 32
+// elements a thread, which do not fit its 64 registers with their weights: 124 to
+// 660 bytes of each thread's go through local memory forward, 540 to 960
+// backward, and the time shows it (4,096 rows with residual, forward and backward:
+// 32,768 bf16 218 and 585 us, 16,384 fp32 364 and 515, where the bytes take 164;
+// 10,001 bf16 576 and 861, where they take 50). Blocks are as many as fit at once; they
 // keep their columns of w in registers, and in the backward pass their columns'
 // sums of dw, written once per block and added in block order by a second
 // kernel. All sums are fp32 in an order fixed by the shape.

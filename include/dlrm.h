@@ -484,9 +484,11 @@ dlrm_status dlrm_dropout(int64_t n, const void* x, const void* residual, dlrm_dt
  *     h may be x's or residual's own buffer
  *   w        fp32 [d], or NULL for ones;  eps >= 0
  *   y        [rows][ld_y] of y_dt: dt, or DLRM_E4M3 with
- *   y_scale  fp32 [rows] (DLRM_E4M3 only): max|y| / 448; the codes are y / y_scale
- *            rounded to nearest. A row of zeros has scale 0 and codes 0; an
- *            infinity or NaN in a row makes its scale one, and with it all of it.
+ *   y_scale  fp32 [rows] (DLRM_E4M3 only): max|y| / 448; the codes are
+ *            y * (448 / max|y|), that factor and the product rounded to fp32,
+ *            rounded to nearest (rows whose max|y| is below 1e-30: y / y_scale).
+ *            A row of zeros has scale 0 and codes 0; an infinity or NaN in a row
+ *            makes its scale one, and with it all of it.
  *   rstd     fp32 [rows], optional (the backward pass takes it) */
 dlrm_status dlrm_rmsnorm_fwd(int rows, int d, const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
                              dlrm_dtype dt, const float* w, float eps, void* h, int64_t ld_h, void* y, int64_t ld_y,
