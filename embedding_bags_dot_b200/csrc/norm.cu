@@ -17,11 +17,12 @@
 // next rows are on their way to shared memory meanwhile. Rows of more than 16,384
 // 16-bit or 8,192 other elements (fp32, and widths without whole runs) take 32
 // elements a thread, which do not fit its 64 registers with their weights: 124 to
-// 660 bytes of each thread's go through local memory forward, 540 to 960
-// backward, and the time shows it (4,096 rows with residual, forward and backward:
-// 32,768 bf16 218 and 585 us, 16,384 fp32 364 and 515, where the bytes take 164;
-// 10,001 bf16 576 and 861, where they take 50). Blocks are as many as fit at once; they
-// keep their columns of w in registers, and in the backward pass their columns'
+// 660 bytes of each thread's go through local memory forward, 540 to 960 backward
+// (76 in the backward pass of 4,097 to 16,384 16-bit columns), and the time shows
+// it (4,096 rows with residual, forward and backward: 32,768 bf16 218 and 585 us,
+// 16,384 fp32 364 and 515, where the bytes take 164; 10,001 bf16 576 and 861,
+// where they take 50). Blocks are as many as fit at once; they keep their columns
+// of w in registers, and in the backward pass their columns'
 // sums of dw, written once per block and added in block order by a second
 // kernel. All sums are fp32 in an order fixed by the shape.
 #include <algorithm>
